@@ -12,6 +12,7 @@ ELEM_E4M3, ELEM_E2M1, ELEM_E5M2 = 0, 1, 2
 SCALE_TENSOR, SCALE_TILE_1x128, SCALE_BLOCK_128x128, SCALE_MX32_E8M0, SCALE_NV16_E4M3 = 0, 1, 2, 3, 4
 ROUND_RNE, ROUND_STOCHASTIC = 0, 1
 OUT_FP32, OUT_BF16 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 TILE_AUTO, TILE_NARROW, TILE_WIDE = 0, 1, 2
 
 EXPORTS = (
@@ -35,6 +36,14 @@ EXPORTS = (
     "fgs_grouped_wgrad_block_scaled",
     "fgs_workspace_bytes",
     "fgs_gemm_workspace_bytes",
+    "fgs_attention_fwd",
+    "fgs_attention_bwd",
+    "fgs_attention_workspace_bytes",
+    "fgs_residual_norm_fwd",
+    "fgs_residual_norm_bwd",
+    "fgs_residual_norm_workspace_bytes",
+    "fgs_clip_grad_norm",
+    "fgs_clip_workspace_bytes",
     "fgs_last_error",
     "fgs_version",
 )
@@ -59,6 +68,14 @@ class FgsGemmOptions(ctypes.Structure):
         ("scales_out", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class FgsHeads(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("ld_token", ctypes.c_int64),
+        ("ld_head", ctypes.c_int64),
     ]
 
 
@@ -106,6 +123,19 @@ def load() -> ctypes.CDLL:
     lib.fgs_workspace_bytes.restype = SZ
     lib.fgs_gemm_workspace_bytes.argtypes = [I32, I64, I64]
     lib.fgs_gemm_workspace_bytes.restype = SZ
+    HP, F32 = ctypes.POINTER(FgsHeads), ctypes.c_float
+    lib.fgs_attention_fwd.argtypes = [HP, HP, HP, P, I32, I64, I32, I32, I32, F32, HP, P, P]
+    lib.fgs_attention_bwd.argtypes = [HP, HP, HP, HP, HP, P, P, I32, I64, I32, I32, I32, F32, HP, HP, HP, P, SZ, P]
+    lib.fgs_attention_workspace_bytes.argtypes = [I64, I32]
+    lib.fgs_attention_workspace_bytes.restype = SZ
+    lib.fgs_residual_norm_fwd.argtypes = [P, I64, P, I64, I32, I64, I64, P, P, I64, I32, F32, P, F32, P, P, P]
+    lib.fgs_residual_norm_bwd.argtypes = [P, I64, P, I64, P, I64, P, I64, I32, I64, I64, P, P, I64, I32, F32, P, F32,
+                                          P, P, P, P, P, P, SZ, P]
+    lib.fgs_residual_norm_workspace_bytes.argtypes = [I64, I64]
+    lib.fgs_residual_norm_workspace_bytes.restype = SZ
+    lib.fgs_clip_grad_norm.argtypes = [P, I32, F32, P, P, SZ, P]
+    lib.fgs_clip_workspace_bytes.argtypes = [I32]
+    lib.fgs_clip_workspace_bytes.restype = SZ
     lib.fgs_last_error.restype = ctypes.c_char_p
     lib.fgs_version.restype = ctypes.c_char_p
     for name in ("fgs_quantize_blockwise", "fgs_quantize_blockwise_noalloc", "fgs_quantize_delayed", "fgs_quantize_mx", "fgs_quantize_nvfp4",
@@ -115,7 +145,8 @@ def load() -> ctypes.CDLL:
                  "fgs_grouped_gemm_block_scaled_fp8mma", "fgs_grouped_wgrad_block_scaled_fp8mma",
                  "fgs_quantize_grouped_colwise", "fgs_grouped_wgrad_block_scaled",
                  "fgs_swiglu_quantize_grouped", "fgs_gemm_block_scaled_fp8out",
-                 "fgs_grouped_gemm_block_scaled_fp8out"):
+                 "fgs_grouped_gemm_block_scaled_fp8out", "fgs_attention_fwd", "fgs_attention_bwd",
+                 "fgs_residual_norm_fwd", "fgs_residual_norm_bwd", "fgs_clip_grad_norm"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

@@ -1,0 +1,120 @@
+"""Causal attention over packed sequences with grouped heads, forward and
+backward (the kernels behind fgs_attention_fwd / fgs_attention_bwd), and its
+autograd form.
+
+A pack holds sequences of different lengths one after the other:
+cu_seqlens (int32 [S + 1] on the GPU) says where each begins and ends, and is
+read on the device, so no call waits for the GPU.  attention_fwd and
+attention_bwd keep no state and can be captured into a graph; so can
+attention(), whose backward pass captures like that of any torch function.
+"""
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .ops import _ptr, _stream
+
+_LIMIT = "must be a [tokens x heads x head_dim] bfloat16 tensor"
+
+
+def _heads(t: torch.Tensor, name: str) -> _lib.FgsHeads:
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise TypeError(f"{name} {_LIMIT}")
+    if not t.is_cuda:
+        raise ValueError("fine_grained_scaled_amd operates on GPU tensors only")
+    token, head, value = t.stride()
+    if value != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride along head_dim")
+    return _lib.FgsHeads(t.data_ptr(), token, head)
+
+
+def _check(q, k, v, cu_seqlens, softmax_scale):
+    T, H, D = q.shape
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k and v must be [{T} x kv_heads x {D}] (got {tuple(k.shape)} and {tuple(v.shape)})")
+    if k.shape[1] == 0 or H % k.shape[1]:
+        raise ValueError(f"heads ({H}) must be a multiple of kv_heads ({k.shape[1]})")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
+            or cu_seqlens.numel() < 1:
+        raise TypeError("cu_seqlens must be a contiguous 1-D int32 tensor of one entry at least")
+    if not (q.device == k.device == v.device == cu_seqlens.device):
+        raise ValueError("q, k, v and cu_seqlens must be on one GPU")
+    return T, H, k.shape[1], D, (1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale))
+
+
+def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                  softmax_scale: Optional[float] = None):
+    """Causal attention of every sequence of the pack: returns (out [T x H x D]
+    bfloat16, lse [H x T] float32, the natural logarithm of the row sums).
+    q is [T x H x D], k and v [T x Hk x D] (H a multiple of Hk, D 64 or 128),
+    views of a fused projection among them.  softmax_scale: 1 / sqrt(D).
+    Tokens of no sequence get out = 0 and lse = -inf."""
+    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    T, H, Hk, D, scale = _check(q, k, v, cu_seqlens, softmax_scale)
+    out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    _lib.check(_lib.load().fgs_attention_fwd(qs, ks, vs, _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, H, Hk, D, scale,
+                                             _heads(out, "out"), _ptr(lse), _stream()))
+    return out, lse
+
+
+def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                  lse: torch.Tensor, cu_seqlens: torch.Tensor, softmax_scale: Optional[float] = None,
+                  workspace: Optional[torch.Tensor] = None):
+    """dq, dk, dv of attention_fwd from its inputs, its out and lse, and dout
+    [T x H x D].  workspace: optional uint8 device scratch of
+    fgs_attention_workspace_bytes() bytes.  The same inputs give the same
+    bits; tokens of no sequence get zeros."""
+    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    os, gs = _heads(out, "out"), _heads(dout, "dout")
+    T, H, Hk, D, scale = _check(q, k, v, cu_seqlens, softmax_scale)
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError(f"out and dout must be {tuple(q.shape)} (got {tuple(out.shape)} and {tuple(dout.shape)})")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (H, T) or not lse.is_contiguous():
+        raise TypeError(f"lse must be a contiguous [{H} x {T}] float32 tensor")
+    if not (out.device == dout.device == lse.device == q.device):
+        raise ValueError("all tensors must be on one GPU")
+    dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k, v))
+    lib = _lib.load()
+    need = lib.fgs_attention_workspace_bytes(T, H)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    _lib.check(lib.fgs_attention_bwd(gs, qs, ks, vs, os, _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, H, Hk,
+                                     D, scale, _heads(dq, "dq"), _heads(dk, "dk"), _heads(dv, "dv"), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream()))
+    return dq, dk, dv
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t itself where the kernels can read it, or else a copy laid out for them."""
+    if t.stride(2) == 1 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0:
+        return t
+    return t.contiguous()
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
+        out, lse = attention_fwd(q, k, v, cu_seqlens, softmax_scale)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+        ctx.scale = softmax_scale
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, cu = ctx.saved_tensors
+        dq, dk, dv = attention_bwd(_rows(dout.to(torch.bfloat16)), q, k, v, out, lse, cu, ctx.scale)
+        return dq, dk, dv, None, None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+              softmax_scale: Optional[float] = None) -> torch.Tensor:
+    """attention_fwd's out with autograd: gradients for q, k and v."""
+    return _Attention.apply(q, k, v, cu_seqlens, softmax_scale)

@@ -1,0 +1,314 @@
+// attention_bwd.hip -- the gradients of causal attention over packed
+// sequences with grouped heads, on gfx950.
+//
+// With p = exp(z - lse) the forward pass's probabilities and
+// delta[t] = sum_d dout[t][d] out[t][d]:
+//   dv[u] = sum_t p[t][u] dout[t]
+//   ds[t][u] = p[t][u] (dout[t] . v[u] - delta[t])
+//   dq[t] = scale sum_u ds[t][u] k[u],  dk[u] = scale sum_t ds[t][u] q[t],
+// t over the tokens that see u and, for dk and dv, over the query heads that
+// share the key head.  p and ds are recomputed in FP32 and rounded to BF16
+// once for the products; all sums are FP32.
+//
+// Two kernels, each with its sums in registers: one owns query rows (dq, and
+// delta), the other owns keys (dk, dv) and walks the query heads of their
+// group.  They compute the scores twice, 14 D operations a pair instead of
+// 10, and in return no sum crosses workgroups: no atomics, no FP32 copy of
+// dq, and the same bits on every run.
+#include "attention_device.h"
+
+namespace fgs {
+
+namespace {
+
+using namespace attn;
+
+constexpr float LOG2E = 1.44269504088896340736f;
+
+struct BwdParams {
+    const uint16_t *q, *k, *v, *o, *dout;
+    uint16_t *dq, *dk, *dv;
+    int64_t q_ld, q_hd, k_ld, k_hd, v_ld, v_hd, o_ld, o_hd, do_ld, do_hd;   // elements
+    int64_t dq_ld, dq_hd, dk_ld, dk_hd, dv_ld, dv_hd;
+    const float* lse;
+    float* ws;            // [H][T] log2 of the row sums, then [H][T] delta
+    const int32_t* cu;
+    int64_t T;
+    int S, H, Hk, tiles, groups, group_heads, hb;
+    float scale;
+};
+
+constexpr int BN = 64;    // keys a tile of the dq kernel
+constexpr int QN = 64;    // query rows a tile of the dk, dv kernel
+constexpr int KN = 128;   // keys a workgroup of it
+
+// dq: 4 waves as in the forward kernel (HB heads x 128 / HB tokens, 32 rows a
+// wave), S^T = K Q^T and dP^T = V dO^T a 32-key step, dQ^T += K^T dS^T.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
+{
+    constexpr int TILE = BN * D * 2;
+    __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int group, tile;
+    {
+        const int b = blockIdx.x, G = p.groups;
+        if (G % 8 == 0) {
+            group = (b & 7) * (G / 8) + (b >> 3) % (G / 8);
+            tile = (b >> 3) / (G / 8);
+        } else {
+            group = b % G;
+            tile = b / G;
+        }
+        tile = p.tiles - 1 - tile;
+    }
+    const int rows = 128 / p.hb;
+    const Where at = find_tile(p.cu, p.S, p.T, rows, tile, lane);
+    const int t0 = at.tile * rows;
+    if (t0 >= at.len) return;
+    const int head = group * p.hb + wave % p.hb;
+    const int w0 = t0 + (wave / p.hb) * 32;
+    const int row = w0 + (lane & 31);
+    const bool write = row < at.len;
+    const int64_t token = at.start + (write ? row : at.len - 1);
+    uint16_t* dq_row = p.dq + token * p.dq_ld + head * p.dq_hd;
+
+    f32x16 dq[D / 32];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
+    if (!at.sequence) {
+        store_row<D>(dq_row, dq, 0.0f, lane, write);
+        return;
+    }
+    const int kv_head = head / p.group_heads;
+    const uint16_t* q_row = p.q + token * p.q_ld + head * p.q_hd;
+    const uint16_t* do_row = p.dout + token * p.do_ld + head * p.do_hd;
+    const uint16_t* o_row = p.o + token * p.o_ld + head * p.o_hd;
+    const uint16_t* k_seq = uniform_ptr(p.k + at.start * p.k_ld + kv_head * p.k_hd);
+    const uint16_t* v_seq = uniform_ptr(p.v + at.start * p.v_ld + kv_head * p.v_hd);
+    bf16x8 q[D / 16], g[D / 16];
+    float delta = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        q[ks] = *reinterpret_cast<const bf16x8*>(q_row + 16 * ks + 8 * half);
+        g[ks] = *reinterpret_cast<const bf16x8*>(do_row + 16 * ks + 8 * half);
+        const bf16x8 o = *reinterpret_cast<const bf16x8*>(o_row + 16 * ks + 8 * half);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) delta = __builtin_fmaf((float)g[ks][j], (float)o[j], delta);
+    }
+    delta += swap_half(delta);
+    // a row whose scores are all -Inf has p = 0
+    float lse2 = p.lse[head * p.T + token] * LOG2E;
+    lse2 = lse2 == -__builtin_inff() ? 0.0f : lse2;
+    if (write && half == 0) {
+        p.ws[head * p.T + token] = lse2;
+        p.ws[(p.H + head) * p.T + token] = delta;
+    }
+
+    const uint32_t base = lds_offset(lds);
+    const int last = at.len - 1;
+    const int n_tiles = (min(t0 + rows, at.len) + BN - 1) / BN;
+    const int wave_keys = w0 < at.len ? min(w0 + 32, at.len) : 0;
+    const float c = p.scale * LOG2E;
+    auto load = [&](int n, int buf) {
+        const int k0 = n * BN;
+        stage<D, BN, 4>(k_seq + (int64_t)k0 * p.k_ld, (uint32_t)p.k_ld * 2, last - k0, base + buf * TILE, wave, lane);
+        stage<D, BN, 4>(v_seq + (int64_t)k0 * p.v_ld, (uint32_t)p.v_ld * 2, last - k0, base + (2 + buf) * TILE, wave,
+                        lane);
+    };
+    load(0, 0);
+    for (int n = 0; n < n_tiles; ++n) {
+        const int buf = n & 1;
+        publish();
+        if (n + 1 < n_tiles) load(n + 1, buf ^ 1);
+        const char* kt = lds + buf * TILE;
+        const char* vt = lds + (2 + buf) * TILE;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int k0 = n * BN + 32 * t;
+            if (k0 >= wave_keys) continue;
+            f32x16 s, dp;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                s = mfma(read_rows<D>(kt, 32 * t, ks, lane), q[ks], s);
+                dp = mfma(read_rows<D>(vt, 32 * t, ks, lane), g[ks], dp);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+            if (k0 + 31 > w0) {
+                const int seen = min(row, last) - k0 - 4 * half;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (acc_row(i, 0) > seen) s[i] = 0.0f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 ds = pack8(s, 8 * ks);
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt)
+                    dq[dt] = mfma(read_tr<D>(kt, 32 * t + 16 * ks, dt, lane), ds, dq[dt]);
+            }
+        }
+    }
+    if (w0 >= at.len) return;
+    store_row<D>(dq_row, dq, p.scale, lane, write);
+}
+
+// dk and dv: 4 waves of 32 keys, whose key and value rows stay in registers;
+// tiles of 64 query rows and their gradients pass through LDS, head after
+// head of the group.  S = Q K^T and dP = dO V^T leave a lane one key and 16
+// queries a step, again the B operands of dV^T += dO^T P and dK^T += Q^T dS.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attention_dkv_kernel(BwdParams p)
+{
+    constexpr int TILE = QN * D * 2;
+    __shared__ __attribute__((aligned(16))) char lds[4 * TILE + 4 * QN * 4];   // Q0 Q1 dO0 dO1, then the row values
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int kv_head, tile;
+    {
+        const int b = blockIdx.x, G = p.Hk;
+        if (G % 8 == 0) {
+            kv_head = (b & 7) * (G / 8) + (b >> 3) % (G / 8);
+            tile = (b >> 3) / (G / 8);
+        } else {
+            kv_head = b % G;
+            tile = b / G;
+        }
+    }
+    const Where at = find_tile(p.cu, p.S, p.T, KN, tile, lane);
+    const int k0 = at.tile * KN;
+    if (k0 >= at.len) return;
+    const int w0 = k0 + wave * 32;
+    const int key = w0 + (lane & 31);
+    const bool write = key < at.len;
+    const int64_t token = at.start + (write ? key : at.len - 1);
+    uint16_t* dk_row = p.dk + token * p.dk_ld + kv_head * p.dk_hd;
+    uint16_t* dv_row = p.dv + token * p.dv_ld + kv_head * p.dv_hd;
+
+    f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
+    if (!at.sequence) {
+        store_row<D>(dk_row, dk, 0.0f, lane, write);
+        store_row<D>(dv_row, dv, 0.0f, lane, write);
+        return;
+    }
+    const uint16_t* k_row = p.k + token * p.k_ld + kv_head * p.k_hd;
+    const uint16_t* v_row = p.v + token * p.v_ld + kv_head * p.v_hd;
+    bf16x8 k[D / 16], v[D / 16];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        k[ks] = *reinterpret_cast<const bf16x8*>(k_row + 16 * ks + 8 * half);
+        v[ks] = *reinterpret_cast<const bf16x8*>(v_row + 16 * ks + 8 * half);
+    }
+
+    const uint32_t base = lds_offset(lds);
+    const float* values = reinterpret_cast<const float*>(lds + 4 * TILE);
+    const int last = at.len - 1;
+    const int q_first = k0 / QN, q_tiles = (at.len + QN - 1) / QN - q_first;
+    const int steps = q_tiles * p.group_heads;
+    const float c = p.scale * LOG2E;
+    auto load = [&](int n, int buf) {
+        const int head = kv_head * p.group_heads + n / q_tiles;
+        const int q0 = (q_first + n % q_tiles) * QN;
+        const uint16_t* q = uniform_ptr(p.q + (at.start + q0) * p.q_ld + head * p.q_hd);
+        const uint16_t* g = uniform_ptr(p.dout + (at.start + q0) * p.do_ld + head * p.do_hd);
+        stage<D, QN, 4>(q, (uint32_t)p.q_ld * 2, last - q0, base + buf * TILE, wave, lane);
+        stage<D, QN, 4>(g, (uint32_t)p.do_ld * 2, last - q0, base + (2 + buf) * TILE, wave, lane);
+        if (wave < 2)
+            g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0), 4 * min(lane, last - q0),
+                   base + 4 * TILE + (2 * buf + wave) * QN * 4);
+    };
+    load(0, 0);
+    for (int n = 0; n < steps; ++n) {
+        const int buf = n & 1;
+        const int q_tile = (q_first + n % q_tiles) * QN;
+        publish();
+        if (n + 1 < steps) load(n + 1, buf ^ 1);
+        const char* qt = lds + buf * TILE;
+        const char* gt = lds + (2 + buf) * TILE;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int q0 = q_tile + 32 * t;
+            if (q0 + 31 < w0 || q0 >= at.len) continue;
+            f32x16 s, dp;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) s = mfma(read_rows<D>(qt, 32 * t, ks, lane), k[ks], s);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) dp = mfma(read_rows<D>(gt, 32 * t, ks, lane), v[ks], dp);
+            const float* lse2 = values + 2 * buf * QN + 32 * t + 4 * half;
+            const float* delta = lse2 + QN;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f32x4 a = *reinterpret_cast<const f32x4*>(lse2 + 2 * i);
+                const f32x4 d = *reinterpret_cast<const f32x4*>(delta + 2 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + j], c, -a[j]));
+                    dp[i + j] = s[i + j] * (dp[i + j] - d[j]);
+                }
+            }
+            if (q0 < w0 + 31 || q0 + 32 > at.len) {
+                const int from = key - q0 - 4 * half, to = at.len - q0 - 4 * half;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (acc_row(i, 0) < from || acc_row(i, 0) >= to) s[i] = dp[i] = 0.0f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 pr = pack8(s, 8 * ks), ds = pack8(dp, 8 * ks);
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt) {
+                    dv[dt] = mfma(read_tr<D>(gt, 32 * t + 16 * ks, dt, lane), pr, dv[dt]);
+                    dk[dt] = mfma(read_tr<D>(qt, 32 * t + 16 * ks, dt, lane), ds, dk[dt]);
+                }
+            }
+        }
+    }
+    if (w0 >= at.len) return;
+    store_row<D>(dk_row, dk, p.scale, lane, write);
+    store_row<D>(dv_row, dv, 1.0f, lane, write);
+}
+
+} // namespace
+
+hipError_t launch_attention_bwd(const AttentionArgs& a, hipStream_t stream)
+{
+    BwdParams p{};
+    p.q = (const uint16_t*)a.q.data, p.k = (const uint16_t*)a.k.data, p.v = (const uint16_t*)a.v.data;
+    p.o = (const uint16_t*)a.out.data, p.dout = (const uint16_t*)a.dout.data;
+    p.dq = (uint16_t*)a.dq.data, p.dk = (uint16_t*)a.dk.data, p.dv = (uint16_t*)a.dv.data;
+    p.q_ld = a.q.ld_token, p.q_hd = a.q.ld_head, p.k_ld = a.k.ld_token, p.k_hd = a.k.ld_head;
+    p.v_ld = a.v.ld_token, p.v_hd = a.v.ld_head, p.o_ld = a.out.ld_token, p.o_hd = a.out.ld_head;
+    p.do_ld = a.dout.ld_token, p.do_hd = a.dout.ld_head, p.dq_ld = a.dq.ld_token, p.dq_hd = a.dq.ld_head;
+    p.dk_ld = a.dk.ld_token, p.dk_hd = a.dk.ld_head, p.dv_ld = a.dv.ld_token, p.dv_hd = a.dv.ld_head;
+    p.lse = a.lse, p.ws = a.delta, p.cu = a.cu_seqlens, p.T = a.T, p.S = a.S, p.H = a.H, p.Hk = a.Hk;
+    p.group_heads = a.H / a.Hk;
+    p.hb = p.group_heads % 4 == 0 ? 4 : p.group_heads % 2 == 0 ? 2 : 1;
+    p.groups = a.H / p.hb;
+    p.tiles = (int)(a.T / (128 / p.hb)) + a.S + 2;
+    p.scale = a.scale;
+    const dim3 grid((unsigned)((int64_t)p.tiles * p.groups));
+    const dim3 grid_kv((unsigned)((a.T / KN + a.S + 2) * a.Hk));
+    if (a.D == 128) {
+        attention_dq_kernel<128><<<grid, 256, 0, stream>>>(p);
+        attention_dkv_kernel<128><<<grid_kv, 256, 0, stream>>>(p);
+    } else {
+        attention_dq_kernel<64><<<grid, 256, 0, stream>>>(p);
+        attention_dkv_kernel<64><<<grid_kv, 256, 0, stream>>>(p);
+    }
+    return hipGetLastError();
+}
+
+} // namespace fgs

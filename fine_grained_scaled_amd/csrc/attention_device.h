@@ -1,0 +1,204 @@
+// attention_device.h -- device helpers shared by the attention kernels:
+// where a workgroup's rows lie in the packed sequences, staging of row tiles
+// in LDS, and the reads of matrix operands from it (internal header of libfgs).
+#pragma once
+
+#include "fgs_device.h"
+#include "fgs_internal.h"
+
+namespace fgs {
+namespace attn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(3))) s16x4* lds_v4;
+
+__device__ __forceinline__ f32x16 mfma(const bf16x8& a, const bf16x8& b, const f32x16& c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The lane halves of a 32x32 accumulator tile: register i of lane l holds
+// column l % 32 and row 8 (i / 4) + 4 (l / 32) + i % 4.
+__device__ __forceinline__ int acc_row(int i, int half) { return 8 * (i >> 2) + 4 * half + (i & 3); }
+
+__device__ __forceinline__ float swap_half(float x)
+{
+    auto r = __builtin_amdgcn_permlane32_swap(as_u32(x), as_u32(x), false, false);
+    return as_f32((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// Eight accumulator registers as the B operand of a 16-deep product whose
+// contraction runs over the accumulator's rows.  Operand slot (half, j) then
+// stands for row 4 half + j (j < 4) or 8 + 4 half + j - 4: the rows that the
+// lane already holds, so nothing crosses lanes; read_tr() below brings the
+// other operand in the same order.
+__device__ __forceinline__ bf16x8 pack8(const f32x16& s, int i0)
+{
+    bf16x8 r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = (__bf16)s[i0 + j];
+    return r;
+}
+
+// ------------------------------------------------------------------------
+// Rows of D bf16 in LDS, D * 2 bytes apart, in 16-byte chunks; chunk c of
+// row r sits in slot c ^ f(r).  f is chosen so that both kinds of read touch
+// every bank once: 16 rows of one chunk (the row-major operand), and 4 rows
+// of 4 neighbouring chunks (the transposed one).
+// ------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ uint32_t swizzle(uint32_t r)
+{
+    return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
+}
+
+// Global -> LDS copies of 16 bytes a lane that pass no register: lane i
+// fills bytes 16 i .. of the wave's 1 KiB span at lds_addr (uniform).  They
+// are issued from assembly so that the compiler does not make every later
+// LDS read wait for them; publish() waits for them by hand.
+__device__ __forceinline__ void g2lds16(const void* base, uint32_t off, uint32_t lds_addr)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_addr) : "memory", "m0");
+}
+__device__ __forceinline__ void g2lds4(const void* base, uint32_t off, uint32_t lds_addr)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_addr) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p)
+{
+    return __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((lds_ptr)p));
+}
+template <class T>
+__device__ __forceinline__ const T* uniform_ptr(const T* q)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(q);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const T*>(((uint64_t)hi << 32) | lo);
+}
+
+// This wave's copies have landed and its LDS reads are done, and so for
+// every other wave of the workgroup.
+__device__ __forceinline__ void publish()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// ROWS rows at `base` (uniform; row stride ld bytes, below 2^24) into LDS at
+// `lds`, split over the workgroup's WAVES waves.  Rows past `last` repeat row
+// `last`, so nothing outside the sequence is read.
+template <int D, int ROWS, int WAVES>
+__device__ __forceinline__ void stage(const void* base, uint32_t ld, int last, uint32_t lds, int wave, int lane)
+{
+    constexpr int SLOTS = D / 8, PER = 64 / SLOTS, N = ROWS / PER / WAVES;
+    static_assert(N * PER * WAVES == ROWS, "whole copies");
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int copy = wave * N + j;
+        const int r = copy * PER + lane / SLOTS;
+        const uint32_t c = (uint32_t)(lane % SLOTS) ^ swizzle<D>(r);
+        g2lds16(base, __umul24((uint32_t)min(r, last), ld) + c * 16, lds + copy * 1024);
+    }
+}
+
+// The row-major operand of rows r0 + l % 32 (r0 a multiple of 16): 8 values
+// of the 16-deep step ks, values 16 ks + 8 (l / 32) .. .
+template <int D>
+__device__ __forceinline__ bf16x8 read_rows(const char* tile, int r0, int ks, int lane)
+{
+    const uint32_t r = r0 + (lane & 31);
+    const uint32_t c = (uint32_t)(2 * ks + (lane >> 5)) ^ swizzle<D>(lane & 31);
+    return *reinterpret_cast<const bf16x8*>(tile + r * (D * 2) + c * 16);
+}
+
+// The transposed operand: columns 32 dt + l % 32 of the tile, contracted
+// over rows r0 .. r0 + 15 (r0 a multiple of 16) in the order of pack8().
+// One ds_read_b64_tr_b16 gives each lane 4 rows of its column: the 16 lanes
+// of a group address 4 rows of 16 columns, 8 bytes each.
+template <int D>
+__device__ __forceinline__ bf16x8 read_tr(const char* tile, int r0, int dt, int lane)
+{
+    const int half = lane >> 5, i = lane & 15;
+    const uint32_t c = 4 * dt + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+    const uint32_t ra = r0 + 4 * half + (i >> 2), rb = ra + 8;
+    const uint32_t fa = swizzle<D>(4 * half + (i >> 2)), fb = swizzle<D>(8 + 4 * half + (i >> 2));
+    union { s16x4 s[2]; bf16x8 v; } u;
+    u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(tile + ra * (D * 2) + (c ^ fa) * 16 + 8 * (i & 1)));
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(tile + rb * (D * 2) + (c ^ fb) * 16 + 8 * (i & 1)));
+    return u.v;
+}
+
+// An accumulator tile set acc[D / 32] (rows: values of the head, column: the
+// lane's row) written as bf16 to one row per lane, times f: the lane halves
+// swap 4-value pieces so that each lane writes 16 bytes.
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t* row, const f32x16* acc, float f, int lane, bool write)
+{
+    const int half = lane >> 5;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = 4 * (g + (k >> 1)) + 2 * (k & 1);
+                bf16x2 p = {(__bf16)(acc[dt][i] * f), (__bf16)(acc[dt][i + 1] * f)};
+                w[k] = __builtin_bit_cast(uint32_t, p);
+            }
+            auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+            auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+            if (write)
+                *reinterpret_cast<uint4*>(row + 32 * dt + 8 * (g + half)) = make_uint4(a[0], b[0], a[1], b[1]);
+        }
+}
+
+// ------------------------------------------------------------------------
+// The packed sequences.  Segment 0 is what lies before cu[0], segment i in
+// 1..S is sequence i - 1 and segment S + 1 what lies after cu[S]; segment i
+// owns the tiles from floor(start_i / rows) + i on, so a tile finds its
+// segment without a scan, and there are at most T / rows + S + 2 tiles.
+// Offsets that decrease or leave [0, T] are clamped: the rows touched stay
+// inside the buffers, whatever cu holds.
+// ------------------------------------------------------------------------
+struct Where {
+    int64_t start;   // first token of the segment
+    int len;         // its tokens
+    int tile;        // this workgroup's tile within it
+    bool sequence;   // a sequence, not what lies outside all of them
+};
+__device__ __forceinline__ int64_t segment_start(const int32_t* cu, int S, int64_t T, int i)
+{
+    if (i == 0) return 0;
+    if (i > S + 1) return T;
+    return min(max((int64_t)cu[i - 1], (int64_t)0), T);
+}
+__device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, int rows, int tile, int lane)
+{
+    // every lane tests one segment: how many start at or before this tile
+    int n = 0;
+    for (int i0 = 0; i0 < S + 2; i0 += 64) {
+        const int i = i0 + lane;
+        const bool before = i < S + 2 && (int)(segment_start(cu, S, T, i) / rows) + i <= tile;
+        n += __popcll(__ballot(before));
+    }
+    const int seg = __builtin_amdgcn_readfirstlane(n - 1);
+    const int64_t a = segment_start(cu, S, T, seg), b = segment_start(cu, S, T, seg + 1);
+    Where w;
+    w.start = __builtin_amdgcn_readfirstlane((int)a);
+    w.tile = __builtin_amdgcn_readfirstlane(tile - ((int)(a / rows) + seg));
+    w.len = __builtin_amdgcn_readfirstlane(b > a && w.tile >= 0 ? (int)(b - a) : 0);
+    w.sequence = seg > 0 && seg <= S;
+    return w;
+}
+
+} // namespace attn
+} // namespace fgs

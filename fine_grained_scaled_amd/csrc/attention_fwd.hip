@@ -1,0 +1,259 @@
+// attention_fwd.hip -- causal attention over packed sequences with grouped
+// heads, forward, on gfx950.
+//
+// For token t of a sequence and query head h, over the tokens u <= t of the
+// same sequence and the key head h / (H / Hk):
+//   z[u] = scale * q[t] . k[u],  out[t] = sum_u softmax(z)[u] v[u],
+//   lse[t] = log sum_u exp z[u].
+// One pass over the keys with a running maximum m and sum l: scores, sums and
+// the output accumulate in FP32; the probabilities are rounded to BF16 once,
+// for the matrix product with v (each at most 2^-8 off, relative).
+//
+// A workgroup of 4 waves owns 128 query rows of one key head: HB query heads
+// of its group times 128 / HB tokens, each wave 32 tokens of one head, so the
+// heads that share keys share the staged tiles and a short sequence wastes
+// at most 31 rows a head.  Tiles of 64 keys and values are staged in LDS, two
+// deep, by copies that pass no register.  The scores are computed transposed,
+// S^T = K Q^T, so a lane holds 32 keys of one query: its maximum and sum need
+// one exchange between lane halves, and its probabilities are already the B
+// operand of O^T = V^T P^T (attention_device.h).
+#include "attention_device.h"
+
+namespace fgs {
+
+namespace {
+
+using namespace attn;
+
+constexpr int BN = 64;             // keys a tile
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float LN2 = 0.69314718055994530942f;
+
+struct FwdParams {
+    const uint16_t *q, *k, *v;
+    uint16_t* o;
+    int64_t q_ld, q_hd, k_ld, k_hd, v_ld, v_hd, o_ld, o_hd;   // elements
+    float* lse;
+    const int32_t* cu;
+    int64_t T;
+    int S, tiles, groups, group_heads, hb;   // groups: workgroups a token tile; hb: query heads a workgroup
+    float scale;
+};
+
+// The wave's rows again, one key at a time and every hidden key left out:
+// for rows whose output came out non-finite, because the tile products below
+// multiply a hidden key's zero probability with its value, and 0 * Inf is
+// NaN.  Here a row depends on the keys it sees and on nothing else.
+template <int D>
+__device__ __forceinline__ void rows_by_key(const FwdParams& p, const uint16_t* q_row, const uint16_t* k_seq,
+                                         const uint16_t* v_seq, uint16_t* o_row, float* lse_at, int row, int keys,
+                                         int lane, bool write)
+{
+    const int half = lane >> 5;
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll 1
+    for (int key = 0; key < keys; ++key) {
+        float dot = 0.0f;
+#pragma unroll 1
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const bf16x8 a = *reinterpret_cast<const bf16x8*>(q_row + 16 * ks + 8 * half);
+            const bf16x8 b = *reinterpret_cast<const bf16x8*>(k_seq + key * p.k_ld + 16 * ks + 8 * half);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot = __builtin_fmaf((float)a[j], (float)b[j], dot);
+        }
+        dot = (dot + swap_half(dot)) * p.scale * LOG2E;
+        if (key > row) continue;
+        // a NaN score makes the row NaN, as the definition does
+        const float top = dot > m || dot != dot ? dot : m;
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+        const float old = __builtin_amdgcn_exp2f(m - base), pr = __builtin_amdgcn_exp2f(dot - base);
+        m = top;
+        l = l * old + pr;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const bf16x4 x = *reinterpret_cast<const bf16x4*>(v_seq + key * p.v_ld + 32 * dt + 8 * g + 4 * half);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[dt][4 * g + j] = o[dt][4 * g + j] * old + pr * (float)x[j];
+            }
+    }
+    store_row<D>(o_row, o, l == 0.0f ? 0.0f : 1.0f / l, lane, write);
+    if (write && half == 0) *lse_at = m * LN2 + __logf(l);
+}
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
+{
+    constexpr int TILE = BN * D * 2;
+    __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // Workgroups go round the 8 XCDs, each with its own L2: with a multiple
+    // of 8 of them a token tile, one XCD keeps the same key heads.  The last
+    // tiles, which see the most keys, go first.
+    int group, tile;
+    {
+        const int b = blockIdx.x, G = p.groups;
+        if (G % 8 == 0) {
+            group = (b & 7) * (G / 8) + (b >> 3) % (G / 8);
+            tile = (b >> 3) / (G / 8);
+        } else {
+            group = b % G;
+            tile = b / G;
+        }
+        tile = p.tiles - 1 - tile;
+    }
+    const int rows = 128 / p.hb;
+    const Where at = find_tile(p.cu, p.S, p.T, rows, tile, lane);
+    const int t0 = at.tile * rows;
+    if (t0 >= at.len) return;
+    const int head = group * p.hb + wave % p.hb;
+    const int w0 = t0 + (wave / p.hb) * 32;          // the wave's first token in the segment
+    const int row = w0 + (lane & 31);
+    const bool write = row < at.len;
+    const int64_t token = at.start + (write ? row : at.len - 1);
+    uint16_t* o_row = p.o + token * p.o_ld + head * p.o_hd;
+    float* lse_at = p.lse + head * p.T + token;
+
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] = 0.0f;
+    if (!at.sequence) {                                // tokens of no sequence see nothing
+        store_row<D>(o_row, o, 0.0f, lane, write);
+        if (write && half == 0) *lse_at = -__builtin_inff();
+        return;
+    }
+
+    const int kv_head = head / p.group_heads;
+    const uint16_t* q_row = p.q + token * p.q_ld + head * p.q_hd;
+    const uint16_t* k_seq = uniform_ptr(p.k + at.start * p.k_ld + kv_head * p.k_hd);
+    const uint16_t* v_seq = uniform_ptr(p.v + at.start * p.v_ld + kv_head * p.v_hd);
+    bf16x8 q[D / 16];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) q[ks] = *reinterpret_cast<const bf16x8*>(q_row + 16 * ks + 8 * half);
+
+    const uint32_t base = lds_offset(lds);
+    const int last = at.len - 1;
+    const int n_tiles = (min(t0 + rows, at.len) + BN - 1) / BN;
+    const int wave_keys = w0 < at.len ? min(w0 + 32, at.len) : 0;     // keys that some row of the wave sees
+    const float c = p.scale * LOG2E;
+    float m = -__builtin_inff(), l = 0.0f;             // maximum of the raw scores; the lane half's sum
+
+    auto load = [&](int n, int buf) {
+        const int k0 = n * BN;
+        stage<D, BN, 4>(k_seq + (int64_t)k0 * p.k_ld, (uint32_t)p.k_ld * 2, last - k0, base + buf * TILE, wave, lane);
+        stage<D, BN, 4>(v_seq + (int64_t)k0 * p.v_ld, (uint32_t)p.v_ld * 2, last - k0, base + (2 + buf) * TILE, wave,
+                        lane);
+    };
+    load(0, 0);
+    for (int n = 0; n < n_tiles; ++n) {
+        const int buf = n & 1, k0 = n * BN;
+        publish();
+        if (n + 1 < n_tiles) load(n + 1, buf ^ 1);
+        if (k0 >= wave_keys) continue;
+        const char* kt = lds + buf * TILE;
+        const char* vt = lds + (2 + buf) * TILE;
+
+        f32x16 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) s[t] = mfma(read_rows<D>(kt, 32 * t, ks, lane), q[ks], s[t]);
+        }
+        if (k0 + BN > w0) {                            // the diagonal: hide the keys after the row
+            const int seen = min(row, last) - k0 - 4 * half;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (32 * t + acc_row(i, 0) > seen) s[t][i] = -__builtin_inff();
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[1][i]);
+        top = fmaxf(top, swap_half(top));
+        // The maximum only has to keep exp2 in range: it moves when a score
+        // passes it by more than a factor of 2^8, so most tiles leave the
+        // output accumulators as they are.
+        if (__any((top - m) * c > 8.0f)) {
+            const float next = fmaxf(m, top);
+            const float safe = next == -__builtin_inff() ? 0.0f : next;
+            const float old = __builtin_amdgcn_exp2f((m - safe) * c);
+            m = next;
+            l *= old;
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[dt][i] *= old;
+        }
+        const float mc = m == -__builtin_inff() ? 0.0f : m * c;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -mc));
+                l += s[t][i];
+            }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 pr = pack8(s[t], 8 * ks);
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt)
+                    o[dt] = mfma(read_tr<D>(vt, 32 * t + 16 * ks, dt, lane), pr, o[dt]);
+            }
+    }
+    if (w0 >= at.len) return;
+    l += swap_half(l);
+    // 0 * x is NaN for a non-finite x and 0 otherwise
+    float bad = 0.0f * l;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad = __builtin_fmaf(0.0f, o[dt][i], bad);
+    bad += swap_half(bad);
+    const bool redo = bad != bad;
+    store_row<D>(o_row, o, l == 0.0f ? 0.0f : 1.0f / l, lane, write && !redo);
+    if (write && !redo && half == 0) *lse_at = m * p.scale + __logf(l);
+    if (__any(write && redo))
+        rows_by_key<D>(p, q_row, k_seq, v_seq, o_row, lse_at, row, wave_keys, lane, write && redo);
+}
+
+} // namespace
+
+hipError_t launch_attention_fwd(const AttentionArgs& a, hipStream_t stream)
+{
+    FwdParams p{};
+    p.q = (const uint16_t*)a.q.data, p.k = (const uint16_t*)a.k.data, p.v = (const uint16_t*)a.v.data;
+    p.o = (uint16_t*)a.out.data;
+    p.q_ld = a.q.ld_token, p.q_hd = a.q.ld_head, p.k_ld = a.k.ld_token, p.k_hd = a.k.ld_head;
+    p.v_ld = a.v.ld_token, p.v_hd = a.v.ld_head, p.o_ld = a.out.ld_token, p.o_hd = a.out.ld_head;
+    p.lse = a.lse, p.cu = a.cu_seqlens, p.T = a.T, p.S = a.S;
+    p.group_heads = a.H / a.Hk;
+    p.hb = p.group_heads % 4 == 0 ? 4 : p.group_heads % 2 == 0 ? 2 : 1;
+    p.groups = a.H / p.hb;
+    p.tiles = (int)(a.T / (128 / p.hb)) + a.S + 2;
+    p.scale = a.scale;
+    const dim3 grid((unsigned)((int64_t)p.tiles * p.groups));
+    if (a.D == 128)
+        attention_fwd_kernel<128><<<grid, 256, 0, stream>>>(p);
+    else
+        attention_fwd_kernel<64><<<grid, 256, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+} // namespace fgs

@@ -1,0 +1,279 @@
+// clip_grad.hip -- the global norm of many gradient tensors and their
+// clipping, on gfx950.
+//
+//   norm = sqrt(sum over all tensors of g^2),
+//   out = g * c,  c = max_norm / norm where norm > max_norm, else 1.
+//
+// Two passes over the data, bound by memory: c depends on every value.  The
+// tensors' addresses travel as kernel arguments, 128 a launch, so a call
+// needs no table on the device and can be captured into a graph.  A tensor is
+// cut into chunks of its 16-byte aligned address range (its first and last
+// vector may be partial), a workgroup takes every gridDim-th chunk.  Squares
+// are summed in FP64, where no FP32 or BF16 gradient overflows or vanishes;
+// each workgroup leaves one partial sum, and every workgroup of the second
+// pass adds the partial sums in the same order: no atomics, the same bits on
+// every run.  The second pass walks the data backwards, from what the first
+// one read last.
+#include <algorithm>
+#include <cmath>
+
+#include "fgs_device.h"
+#include "fgs_internal.h"
+
+namespace fgs {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int PER_LAUNCH = 128;
+constexpr int PARTS = 1024;              // partial sums a launch at most
+
+struct Table {
+    const void* data[PER_LAUNCH];
+    void* out[PER_LAUNCH];
+    int64_t count[PER_LAUNCH];           // elements; negative: BF16
+    uint32_t first[PER_LAUNCH];          // first chunk
+    uint32_t chunks, tensors;
+    uint32_t chunk_vecs;                 // 16-byte vectors a chunk
+};
+
+// the tensor that owns a chunk: the last one that starts at or before it
+__device__ __forceinline__ int owner(const Table& t, uint32_t chunk)
+{
+    const uint32_t lane = threadIdx.x & 63;
+    int n = 0;
+#pragma unroll
+    for (int i0 = 0; i0 < PER_LAUNCH; i0 += 64)
+        n += __popcll(__ballot(i0 + lane < t.tensors && t.first[i0 + lane] <= chunk));
+    return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+    return v;
+}
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double s[THREADS / 64];
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int w = 0; w < THREADS / 64; ++w) v += s[w];
+    return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void values(const uint4& v, float f[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
+        else f[i] = as_f32(w[i]);
+    }
+}
+
+// the squares of elements e0 + tid * N .. of a chunk, e0 and e1 relative to
+// the tensor's aligned address, the tensor being elements [lo, hi) of it
+template <bool BF16>
+__device__ __forceinline__ double chunk_squares(const char* base, int64_t vec0, uint32_t vecs, int64_t lo, int64_t hi)
+{
+    constexpr int N = BF16 ? 8 : 4;
+    double sum = 0.0;
+    if (vec0 * N >= lo && (vec0 + vecs) * N <= hi && vecs % (4 * THREADS) == 0) {
+        const uint4* p = reinterpret_cast<const uint4*>(base) + vec0 + threadIdx.x;
+        for (uint32_t i = 0; i < vecs; i += 4 * THREADS) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = p[i + k * THREADS];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[8];
+                values<BF16>(v[k], f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) sum = __builtin_fma((double)f[j], (double)f[j], sum);
+            }
+        }
+        return sum;
+    }
+    for (uint32_t i = threadIdx.x; i < vecs; i += THREADS) {
+        const int64_t e = (vec0 + i) * N;
+        if (e >= lo && e + N <= hi) {
+            float f[8];
+            values<BF16>(reinterpret_cast<const uint4*>(base)[vec0 + i], f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum = __builtin_fma((double)f[j], (double)f[j], sum);
+        } else {
+            for (int64_t k = max(e, lo); k < min(e + N, hi); ++k) {
+                const float f = BF16 ? as_f32((uint32_t)reinterpret_cast<const uint16_t*>(base)[k] << 16)
+                                     : reinterpret_cast<const float*>(base)[k];
+                sum = __builtin_fma((double)f, (double)f, sum);
+            }
+        }
+    }
+    return sum;
+}
+
+__global__ __launch_bounds__(THREADS) void grad_squares_kernel(Table t, double* partial)
+{
+    double sum = 0.0;
+    for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+        const int i = owner(t, c);
+        const uint64_t at = (uint64_t)t.data[i];
+        const char* base = (const char*)(at & ~(uint64_t)15);
+        const bool bf16 = t.count[i] < 0;
+        const int64_t n = bf16 ? -t.count[i] : t.count[i];
+        const int64_t lo = (at & 15) / (bf16 ? 2 : 4);
+        const int64_t vec0 = (int64_t)(c - t.first[i]) * t.chunk_vecs;
+        if (bf16) sum += chunk_squares<true>(base, vec0, t.chunk_vecs, lo, lo + n);
+        else sum += chunk_squares<false>(base, vec0, t.chunk_vecs, lo, lo + n);
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 scaled(const uint4& v, float c)
+{
+    float f[8];
+    values<BF16>(v, f);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            const bf16x2 p = {(__bf16)(f[2 * i] * c), (__bf16)(f[2 * i + 1] * c)};
+            w[i] = __builtin_bit_cast(uint32_t, p);
+        } else {
+            w[i] = as_u32(f[i] * c);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void chunk_scale(const char* base, char* out, bool same, int64_t vec0, uint32_t vecs,
+                                            int64_t lo, int64_t hi, float c)
+{
+    constexpr int N = BF16 ? 8 : 4;
+    if (same && vec0 * N >= lo && (vec0 + vecs) * N <= hi && vecs % (4 * THREADS) == 0) {
+        const uint4* p = reinterpret_cast<const uint4*>(base) + vec0 + threadIdx.x;
+        uint4* q = reinterpret_cast<uint4*>(out) + vec0 + threadIdx.x;
+        for (uint32_t i = 0; i < vecs; i += 4 * THREADS) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = p[i + k * THREADS];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[i + k * THREADS] = scaled<BF16>(v[k], c);
+        }
+        return;
+    }
+    for (uint32_t i = threadIdx.x; i < vecs; i += THREADS) {
+        const int64_t e = (vec0 + i) * N;
+        if (e >= lo && e + N <= hi) {
+            const uint4 v = scaled<BF16>(reinterpret_cast<const uint4*>(base)[vec0 + i], c);
+            if (same) {
+                reinterpret_cast<uint4*>(out)[vec0 + i] = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (BF16) reinterpret_cast<uint16_t*>(out)[e + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+                    else reinterpret_cast<uint32_t*>(out)[e + j] = w[j];
+                }
+            }
+        } else {
+            for (int64_t k = max(e, lo); k < min(e + N, hi); ++k) {
+                if (BF16) {
+                    const float f = as_f32((uint32_t)reinterpret_cast<const uint16_t*>(base)[k] << 16) * c;
+                    reinterpret_cast<uint16_t*>(out)[k] = __builtin_bit_cast(uint16_t, (__bf16)f);
+                } else {
+                    reinterpret_cast<float*>(out)[k] = reinterpret_cast<const float*>(base)[k] * c;
+                }
+            }
+        }
+    }
+}
+
+__global__ __launch_bounds__(THREADS) void grad_scale_kernel(Table t, const double* partial, int parts, float max_norm,
+                                                             float* norm_out)
+{
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < parts; i += THREADS) sum += partial[i];
+    const double norm = sqrt(block_sum(sum));
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+    // NaN gives NaN, as the definition does
+    const float c = norm <= (double)max_norm ? 1.0f : (float)((double)max_norm / norm);
+    for (uint32_t b = blockIdx.x; b < t.chunks; b += gridDim.x) {
+        const uint32_t chunk = t.chunks - 1 - b;
+        const int i = owner(t, chunk);
+        const uint64_t at = (uint64_t)t.data[i], to = (uint64_t)t.out[i];
+        if (at == to && c == 1.0f) continue;
+        const bool bf16 = t.count[i] < 0;
+        const int64_t n = bf16 ? -t.count[i] : t.count[i];
+        const int64_t lo = (at & 15) / (bf16 ? 2 : 4);
+        const int64_t vec0 = (int64_t)(chunk - t.first[i]) * t.chunk_vecs;
+        const char* base = (const char*)(at & ~(uint64_t)15);
+        char* out = (char*)to - (at & 15);
+        const bool same = ((at ^ to) & 15) == 0;
+        if (bf16) chunk_scale<true>(base, out, same, vec0, t.chunk_vecs, lo, lo + n, c);
+        else chunk_scale<false>(base, out, same, vec0, t.chunk_vecs, lo, lo + n, c);
+    }
+}
+
+} // namespace
+
+size_t clip_workspace_bytes(int32_t count)
+{
+    return sizeof(double) * PARTS * (size_t)std::max(1, (count + PER_LAUNCH - 1) / PER_LAUNCH);
+}
+
+hipError_t launch_clip_grad_norm(const fgs_grad* grads, int32_t count, float max_norm, float* norm, double* partial,
+                                 hipStream_t stream)
+{
+    int64_t bytes = 0;
+    for (int i = 0; i < count; ++i) bytes += grads[i].count * (grads[i].elem == FGS_OUT_BF16 ? 2 : 4);
+    // 16 KiB chunks spread a small call over the chip; 64 KiB ones find their
+    // tensor less often in a large one
+    const uint32_t vecs = bytes > ((int64_t)64 << 20) ? 4096 : 1024;
+    const int launches = std::max(1, (count + PER_LAUNCH - 1) / PER_LAUNCH);
+    auto fill = [&](Table& t, int launch) {
+        t.chunks = t.tensors = 0;
+        t.chunk_vecs = vecs;
+        const int end = std::min(count, (launch + 1) * PER_LAUNCH);
+        for (int i = launch * PER_LAUNCH; i < end; ++i) {
+            const fgs_grad& g = grads[i];
+            if (g.count == 0) continue;
+            const bool bf16 = g.elem == FGS_OUT_BF16;
+            const int64_t span = (int64_t)((uint64_t)g.data & 15) + g.count * (bf16 ? 2 : 4);
+            t.data[t.tensors] = g.data;
+            t.out[t.tensors] = g.out;
+            t.count[t.tensors] = bf16 ? -g.count : g.count;
+            t.first[t.tensors++] = t.chunks;
+            t.chunks += (uint32_t)((span + 16 * (int64_t)vecs - 1) / (16 * (int64_t)vecs));
+        }
+    };
+    Table t;
+    int parts = 0;
+    for (int k = 0; k < launches; ++k) {
+        fill(t, k);
+        if (t.chunks == 0) continue;
+        const int grid = (int)std::min<uint32_t>(t.chunks, PARTS);
+        grad_squares_kernel<<<grid, THREADS, 0, stream>>>(t, partial + parts);
+        parts += grid;
+    }
+    bool wrote = false;
+    for (int k = launches - 1; k >= 0; --k) {
+        fill(t, k);
+        if (t.chunks == 0 && (k > 0 || wrote)) continue;
+        const int grid = (int)std::max<uint32_t>(1, std::min<uint32_t>(t.chunks, 2048));
+        grad_scale_kernel<<<grid, THREADS, 0, stream>>>(t, partial, parts, max_norm, wrote ? nullptr : norm);
+        wrote = true;
+    }
+    return hipGetLastError();
+}
+
+} // namespace fgs

@@ -547,4 +547,199 @@ int fgs_grouped_wgrad_block_scaled_fp8mma(const fgs_operand* A, const fgs_operan
     return wgrad_impl(A, B, group_offsets, G, total_T, M, N, C, ldc, out_dtype, stream, true);
 }
 
+static int check_heads(const fgs_heads* x, const char* name, int heads, int D, bool output)
+{
+    if (!x) return fail(FGS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!x->data) return fail(FGS_ERR_INVALID_ARG, "%s.data is NULL", name);
+    if (x->ld_token < 0 || x->ld_head < 0) return fail(FGS_ERR_INVALID_ARG, "%s has a negative stride", name);
+    if (!aligned(x->data, 16) || x->ld_token % 8 || x->ld_head % 8)
+        return fail(FGS_ERR_UNSUPPORTED, "%s must be 16-byte aligned with strides that are multiples of 8", name);
+    // a tile's rows are addressed by 24-bit products of row and byte stride
+    if (x->ld_token >= (int64_t)1 << 23) return fail(FGS_ERR_UNSUPPORTED, "%s.ld_token must be below 2^23", name);
+    if (output && (x->ld_token < D || (heads > 1 && x->ld_head < D)))
+        return fail(FGS_ERR_INVALID_ARG, "%s is written and its rows must not overlap (strides below head_dim %d)", name, D);
+    return FGS_OK;
+}
+
+static int check_attention(const int32_t* cu, int32_t S, int64_t T, int32_t H, int32_t Hk, int32_t D, float scale)
+{
+    if (T < 0 || S < 0) return fail(FGS_ERR_INVALID_ARG, "tokens (%lld) and num_seqs (%d) must be >= 0", (long long)T, S);
+    if (H < 1 || Hk < 1 || H % Hk)
+        return fail(FGS_ERR_INVALID_ARG, "heads (%d) must be a positive multiple of kv_heads (%d)", H, Hk);
+    if (D != 64 && D != 128) return fail(FGS_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", D);
+    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(FGS_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (T == 0) return FGS_OK;
+    if (!cu || !aligned(cu, 4)) return fail(FGS_ERR_INVALID_ARG, "cu_seqlens must be a 4-byte aligned device pointer");
+    if (T > 0x7FFFFFFF - 256) return fail(FGS_ERR_UNSUPPORTED, "tokens too large (%lld)", (long long)T);
+    if (S > (1 << 24) || (T / 32 + S + 2) * H > 0x7FFFFFFF) return fail(FGS_ERR_UNSUPPORTED, "too many tiles");
+    return FGS_OK;
+}
+
+int fgs_attention_fwd(const fgs_heads* q, const fgs_heads* k, const fgs_heads* v,
+                      const int32_t* cu_seqlens, int32_t num_seqs, int64_t tokens,
+                      int32_t heads, int32_t kv_heads, int32_t head_dim, float scale,
+                      const fgs_heads* out, float* lse, void* stream)
+{
+    int st = check_attention(cu_seqlens, num_seqs, tokens, heads, kv_heads, head_dim, scale);
+    if (st != FGS_OK) return st;
+    if (tokens == 0) return ok();
+    if ((st = check_heads(q, "q", heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(k, "k", kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(v, "v", kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(out, "out", heads, head_dim, true)) != FGS_OK) return st;
+    if (!lse || !aligned(lse, 4)) return fail(FGS_ERR_INVALID_ARG, "lse must be a 4-byte aligned device pointer");
+    fgs::AttentionArgs a{};
+    a.q = *q, a.k = *k, a.v = *v, a.out = *out, a.lse = lse, a.cu_seqlens = cu_seqlens;
+    a.T = tokens, a.S = num_seqs, a.H = heads, a.Hk = kv_heads, a.D = head_dim, a.scale = scale;
+    return hip_status(fgs::launch_attention_fwd(a, static_cast<hipStream_t>(stream)), "attention_fwd launch");
+}
+
+size_t fgs_attention_workspace_bytes(int64_t tokens, int32_t heads)
+{
+    if (tokens < 0 || heads < 0) return 0;
+    return (size_t)tokens * heads * 8;
+}
+
+int fgs_attention_bwd(const fgs_heads* dout, const fgs_heads* q, const fgs_heads* k, const fgs_heads* v,
+                      const fgs_heads* out, const float* lse,
+                      const int32_t* cu_seqlens, int32_t num_seqs, int64_t tokens,
+                      int32_t heads, int32_t kv_heads, int32_t head_dim, float scale,
+                      const fgs_heads* dq, const fgs_heads* dk, const fgs_heads* dv,
+                      void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_attention(cu_seqlens, num_seqs, tokens, heads, kv_heads, head_dim, scale);
+    if (st != FGS_OK) return st;
+    if (tokens == 0) return ok();
+    if ((st = check_heads(dout, "dout", heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(q, "q", heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(k, "k", kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(v, "v", kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(out, "out", heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(dq, "dq", heads, head_dim, true)) != FGS_OK) return st;
+    if ((st = check_heads(dk, "dk", kv_heads, head_dim, true)) != FGS_OK) return st;
+    if ((st = check_heads(dv, "dv", kv_heads, head_dim, true)) != FGS_OK) return st;
+    if (!lse || !aligned(lse, 4)) return fail(FGS_ERR_INVALID_ARG, "lse must be a 4-byte aligned device pointer");
+    const size_t need = fgs_attention_workspace_bytes(tokens, heads);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+        return fail(FGS_ERR_INVALID_ARG, "attention_bwd needs a 16-byte aligned workspace of %zu bytes", need);
+    fgs::AttentionArgs a{};
+    a.q = *q, a.k = *k, a.v = *v, a.out = *out, a.dout = *dout, a.dq = *dq, a.dk = *dk, a.dv = *dv;
+    a.lse = const_cast<float*>(lse), a.delta = static_cast<float*>(workspace), a.cu_seqlens = cu_seqlens;
+    a.T = tokens, a.S = num_seqs, a.H = heads, a.Hk = kv_heads, a.D = head_dim, a.scale = scale;
+    return hip_status(fgs::launch_attention_bwd(a, static_cast<hipStream_t>(stream)), "attention_bwd launch");
+}
+
+static int check_rows(const void* p, int64_t ld, int64_t width, const char* name)
+{
+    if (!p) return fail(FGS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (ld < width) return fail(FGS_ERR_INVALID_ARG, "%s: row stride %lld < width %lld", name, (long long)ld, (long long)width);
+    if (ld % 8 || !aligned(p, 16)) return fail(FGS_ERR_UNSUPPORTED, "%s must be 16-byte aligned with a row stride that is a multiple of 8", name);
+    return FGS_OK;
+}
+
+static int check_norm(int residual_dtype, int64_t rows, int64_t width, const float* w_post, const void* gate,
+                      int64_t ldg, int gate_kind, float alpha, const float* w_pre, float eps)
+{
+    if (residual_dtype != FGS_OUT_FP32 && residual_dtype != FGS_OUT_BF16)
+        return fail(FGS_ERR_INVALID_ARG, "residual_dtype %d is not FGS_OUT_FP32 or FGS_OUT_BF16", residual_dtype);
+    if (gate_kind < FGS_GATE_NONE || gate_kind > FGS_GATE_TOKEN) return fail(FGS_ERR_INVALID_ARG, "gate_kind %d invalid", gate_kind);
+    if (rows < 0 || width < 1) return fail(FGS_ERR_INVALID_ARG, "rows (%lld) must be >= 0 and width (%lld) >= 1", (long long)rows, (long long)width);
+    if (width % 8 || width > 16384) return fail(FGS_ERR_UNSUPPORTED, "width must be a multiple of 8, at most 16384 (got %lld)", (long long)width);
+    if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(FGS_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!(alpha - alpha == 0.0f)) return fail(FGS_ERR_INVALID_ARG, "alpha must be finite");
+    if (rows == 0) return FGS_OK;
+    if (!w_pre || !aligned(w_pre, 16)) return fail(FGS_ERR_INVALID_ARG, "w_pre must be a 16-byte aligned device pointer");
+    if (w_post && !aligned(w_post, 16)) return fail(FGS_ERR_UNSUPPORTED, "w_post must be 16-byte aligned");
+    if (gate_kind == FGS_GATE_CHANNEL && (!gate || !aligned(gate, 16))) return fail(FGS_ERR_INVALID_ARG, "gate must be a 16-byte aligned device pointer");
+    if (gate_kind == FGS_GATE_TOKEN) return check_rows(gate, ldg, width, "gate");
+    return FGS_OK;
+}
+
+int fgs_residual_norm_fwd(const void* y, int64_t ldy, const void* x, int64_t ldx, int residual_dtype,
+                          int64_t rows, int64_t width, const float* w_post,
+                          const void* gate, int64_t ldg, int gate_kind, float alpha,
+                          const float* w_pre, float eps, void* r, void* n, void* stream)
+{
+    int st = check_norm(residual_dtype, rows, width, w_post, gate, ldg, gate_kind, alpha, w_pre, eps);
+    if (st != FGS_OK) return st;
+    if (rows == 0) return ok();
+    if ((st = check_rows(y, ldy, width, "y")) != FGS_OK) return st;
+    if ((st = check_rows(x, ldx, width, "x")) != FGS_OK) return st;
+    if ((st = check_rows(r, width, width, "r")) != FGS_OK) return st;
+    if ((st = check_rows(n, width, width, "n")) != FGS_OK) return st;
+    fgs::NormArgs a{};
+    a.T = rows, a.W = width, a.y = y, a.x = x, a.gate = gate, a.ldy = ldy, a.ldx = ldx, a.ldg = ldg;
+    a.fp32 = residual_dtype == FGS_OUT_FP32, a.gate_kind = gate_kind, a.w_post = w_post, a.w_pre = w_pre;
+    a.alpha = alpha, a.eps = eps, a.r = r, a.n = n;
+    return hip_status(fgs::launch_residual_norm_fwd(a, static_cast<hipStream_t>(stream)), "residual_norm_fwd launch");
+}
+
+size_t fgs_residual_norm_workspace_bytes(int64_t rows, int64_t width)
+{
+    if (rows < 0 || width < 1 || width > 16384) return 0;
+    return (size_t)fgs::residual_norm_parts(rows, width) * 3 * (size_t)width * sizeof(float) + 16;
+}
+
+int fgs_residual_norm_bwd(const void* dr, int64_t lddr, const void* dn, int64_t lddn,
+                          const void* y, int64_t ldy, const void* r, int64_t ldr, int residual_dtype,
+                          int64_t rows, int64_t width, const float* w_post,
+                          const void* gate, int64_t ldg, int gate_kind, float alpha,
+                          const float* w_pre, float eps,
+                          void* dx, void* dy, void* dgate, float* dw_post, float* dw_pre,
+                          void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_norm(residual_dtype, rows, width, w_post, gate, ldg, gate_kind, alpha, w_pre, eps);
+    if (st != FGS_OK) return st;
+    if (!dw_pre || !aligned(dw_pre, 4)) return fail(FGS_ERR_INVALID_ARG, "dw_pre must be a 4-byte aligned device pointer");
+    if (w_post && (!dw_post || !aligned(dw_post, 4))) return fail(FGS_ERR_INVALID_ARG, "dw_post must be a 4-byte aligned device pointer");
+    if (gate_kind == FGS_GATE_CHANNEL && (!dgate || !aligned(dgate, 4))) return fail(FGS_ERR_INVALID_ARG, "dgate must be a 4-byte aligned device pointer");
+    if (rows > 0) {
+        if ((st = check_rows(dr, lddr, width, "dr")) != FGS_OK) return st;
+        if ((st = check_rows(dn, lddn, width, "dn")) != FGS_OK) return st;
+        if ((st = check_rows(y, ldy, width, "y")) != FGS_OK) return st;
+        if ((st = check_rows(r, ldr, width, "r")) != FGS_OK) return st;
+        if ((st = check_rows(dx, width, width, "dx")) != FGS_OK) return st;
+        if ((st = check_rows(dy, width, width, "dy")) != FGS_OK) return st;
+        if (gate_kind == FGS_GATE_TOKEN && (st = check_rows(dgate, width, width, "dgate")) != FGS_OK) return st;
+    }
+    const size_t need = fgs_residual_norm_workspace_bytes(rows, width);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+        return fail(FGS_ERR_INVALID_ARG, "residual_norm_bwd needs a 16-byte aligned workspace of %zu bytes", need);
+    fgs::NormArgs a{};
+    a.T = rows, a.W = width, a.y = y, a.x = r, a.gate = gate, a.ldy = ldy, a.ldx = ldr, a.ldg = ldg;
+    a.fp32 = residual_dtype == FGS_OUT_FP32, a.gate_kind = gate_kind, a.w_post = w_post, a.w_pre = w_pre;
+    a.alpha = alpha, a.eps = eps, a.dr = dr, a.dn = dn, a.lddr = lddr, a.lddn = lddn;
+    a.dx = dx, a.dy = dy, a.dgate = dgate, a.dw_post = dw_post, a.dw_pre = dw_pre;
+    a.partial = static_cast<float*>(workspace);
+    return hip_status(fgs::launch_residual_norm_bwd(a, static_cast<hipStream_t>(stream)), "residual_norm_bwd launch");
+}
+
+size_t fgs_clip_workspace_bytes(int32_t count) { return count < 0 ? 0 : fgs::clip_workspace_bytes(count); }
+
+int fgs_clip_grad_norm(const fgs_grad* grads, int32_t count, float max_norm, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (count < 0) return fail(FGS_ERR_INVALID_ARG, "count (%d) must be >= 0", count);
+    if (count > 0 && !grads) return fail(FGS_ERR_INVALID_ARG, "grads is NULL");
+    if (!(max_norm >= 0.0f)) return fail(FGS_ERR_INVALID_ARG, "max_norm must be >= 0");
+    if (!norm || !aligned(norm, 4)) return fail(FGS_ERR_INVALID_ARG, "norm must be a 4-byte aligned device pointer");
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < fgs_clip_workspace_bytes(count))
+        return fail(FGS_ERR_INVALID_ARG, "clip_grad_norm needs a 16-byte aligned workspace of %zu bytes",
+                    fgs_clip_workspace_bytes(count));
+    int64_t chunks = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const fgs_grad& g = grads[i];
+        if (g.elem != FGS_OUT_FP32 && g.elem != FGS_OUT_BF16) return fail(FGS_ERR_INVALID_ARG, "grads[%d].elem %lld invalid", i, (long long)g.elem);
+        if (g.count < 0 || g.count > (int64_t)1 << 40) return fail(FGS_ERR_INVALID_ARG, "grads[%d].count %lld invalid", i, (long long)g.count);
+        if (g.count == 0) continue;
+        const size_t size = g.elem == FGS_OUT_BF16 ? 2 : 4;
+        if (!g.data || !g.out) return fail(FGS_ERR_INVALID_ARG, "grads[%d] has a NULL pointer", i);
+        if (!aligned(g.data, size) || !aligned(g.out, size)) return fail(FGS_ERR_UNSUPPORTED, "grads[%d] is not aligned to its values", i);
+        chunks += (int64_t)(g.count * size) / 16384 + 2;
+    }
+    if (chunks > 0x7FFFFFFF) return fail(FGS_ERR_UNSUPPORTED, "too many values");
+    return hip_status(fgs::launch_clip_grad_norm(grads, count, max_norm, norm, static_cast<double*>(workspace),
+                                                 static_cast<hipStream_t>(stream)), "clip_grad_norm launch");
+}
+
 } // extern "C"

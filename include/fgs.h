@@ -511,6 +511,142 @@ int fgs_gemm_block_scaled_ex(const fgs_operand *A, const fgs_operand *B,
 int fgs_gemm_kernel_name(const fgs_operand *A, const fgs_operand *B, int64_t M, int64_t N, int64_t K,
                          int out_dtype, const fgs_gemm_options *opts, char *name, size_t len);
 
+/*
+ * The operators around a transformer block's linear layers: causal attention
+ * over packed sequences, the block boundary (norms, gate and residual) and
+ * the global gradient norm with clipping, each in BF16 with FP32 statistics
+ * and sums.  They are not on the pages: a block trained with the GEMMs above
+ * runs them in higher precision ([DSV3] "Mixed precision framework" keeps
+ * attention and normalisation out of FP8).
+ */
+
+/* Heads of head_dim BF16 values: value d of head h of token t is at
+ * data + t * ld_token + h * ld_head + d (elements).  A slice of a fused
+ * projection's output is given by its pointer and strides. */
+typedef struct {
+    const void *data;   /* device; the entry point says whether it is written */
+    int64_t ld_token;
+    int64_t ld_head;
+} fgs_heads;
+
+/*
+ * fgs_attention_fwd -- causal attention over packed sequences with grouped
+ *   heads.  For token t of a sequence, query head h and key head
+ *   h / (heads / kv_heads), over the tokens u <= t of the same sequence:
+ *   z[u] = scale * q[t].k[u], out[t] = sum_u softmax(z)[u] v[u],
+ *   lse[h][t] = log(sum_u exp(z[u])) (natural logarithm).
+ * q, out   heads x head_dim per token; k, v: kv_heads x head_dim.  Pointers
+ *          16-byte aligned, strides multiples of 8, ld_token < 2^23.
+ * cu_seqlens  DEVICE int32 [num_seqs + 1], non-decreasing, in [0, tokens]:
+ *          sequence s is tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (none
+ *          is allowed).  Read on the device (no host synchronisation).
+ *          Tokens of no sequence get out = 0 and lse = -Inf.  Offsets that
+ *          decrease give unspecified values, but every access stays inside
+ *          the tensors.
+ * lse      FP32 [heads][tokens].
+ * head_dim 64 or 128; heads a multiple of kv_heads; scale finite and > 0.
+ * Scores, softmax statistics and sums are FP32; the probabilities are rounded
+ * to BF16 for the product with v.  A row depends on the tokens it sees alone:
+ * NaN or Inf in later tokens or other sequences do not reach it.  A row whose
+ * scores are all -Inf gets out = 0 and lse = -Inf.
+ */
+int fgs_attention_fwd(const fgs_heads *q, const fgs_heads *k, const fgs_heads *v,
+                      const int32_t *cu_seqlens, int32_t num_seqs, int64_t tokens,
+                      int32_t heads, int32_t kv_heads, int32_t head_dim, float scale,
+                      const fgs_heads *out, float *lse, void *stream);
+
+/*
+ * fgs_attention_bwd -- the gradients dq, dk, dv of fgs_attention_fwd from its
+ *   inputs, its out and lse, and dout.  dk and dv sum over the query heads
+ *   that share a key head.  Tokens of no sequence get zeros.  The sums have a
+ *   fixed order (no atomics): the same inputs give the same bits.  NaN or Inf
+ *   in one sequence do not reach another; within one they may reach up to 127
+ *   neighbouring rows that the mask hides from them.
+ * Layouts, cu_seqlens and limits as fgs_attention_fwd.
+ * workspace  DEVICE scratch, 16-byte aligned, of at least
+ *   fgs_attention_workspace_bytes(tokens, heads) bytes.
+ */
+int fgs_attention_bwd(const fgs_heads *dout, const fgs_heads *q, const fgs_heads *k, const fgs_heads *v,
+                      const fgs_heads *out, const float *lse,
+                      const int32_t *cu_seqlens, int32_t num_seqs, int64_t tokens,
+                      int32_t heads, int32_t kv_heads, int32_t head_dim, float scale,
+                      const fgs_heads *dq, const fgs_heads *dk, const fgs_heads *dv,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace of fgs_attention_bwd: two FP32 values a head and token
+ * (0 for negative arguments). */
+size_t fgs_attention_workspace_bytes(int64_t tokens, int32_t heads);
+
+/*
+ * fgs_residual_norm_fwd -- the boundary between two blocks in one pass: norm
+ *   of the block's output, gate, scaled residual, norm for the next block.
+ *     z = y / rms(y) * w_post            (z = y if w_post is NULL)
+ *     r = alpha * x + gate * z           rounded to the residual's type
+ *     n = r / rms(r) * w_pre             of the rounded r
+ *   rms(t) = sqrt(mean over the row of t^2 + eps).
+ * y        BF16 [rows x width], row stride ldy.
+ * x, r     the residual stream, FP32 or BF16 (residual_dtype FGS_OUT_FP32 |
+ *          FGS_OUT_BF16); x has row stride ldx, r is dense.
+ * gate     by gate_kind: FGS_GATE_NONE (NULL, 1), FGS_GATE_CHANNEL (FP32
+ *          [width]), FGS_GATE_TOKEN (BF16 [rows x width], row stride ldg).
+ * w_post, w_pre  FP32 [width]; w_post may be NULL.
+ * n        BF16 [rows x width], dense.
+ * width and strides are multiples of 8, width <= 16384; pointers 16-byte
+ * aligned; eps >= 0.  x and r, or y and n, may be the same tensor (dense).
+ * Statistics and sums are FP32; rows = 0 does nothing.
+ */
+enum { FGS_GATE_NONE = 0, FGS_GATE_CHANNEL = 1, FGS_GATE_TOKEN = 2 };
+int fgs_residual_norm_fwd(const void *y, int64_t ldy, const void *x, int64_t ldx, int residual_dtype,
+                          int64_t rows, int64_t width, const float *w_post,
+                          const void *gate, int64_t ldg, int gate_kind, float alpha,
+                          const float *w_pre, float eps, void *r, void *n, void *stream);
+
+/*
+ * fgs_residual_norm_bwd -- the gradients of fgs_residual_norm_fwd from y, the
+ *   r it returned (row stride ldr), and the gradients dr (residual type) and
+ *   dn (BF16) of its two outputs.
+ * dx       residual type, dense; dy: BF16, dense.
+ * dgate    FP32 [width] (channel), BF16 [rows x width] dense (token), ignored
+ *          without a gate.
+ * dw_post, dw_pre  FP32 [width]; dw_post is ignored if w_post is NULL.
+ * The sums over rows have a fixed order (no atomics).  rows = 0 writes zeros
+ * to the sums.
+ * workspace  DEVICE scratch, 16-byte aligned, of at least
+ *   fgs_residual_norm_workspace_bytes(rows, width) bytes.
+ */
+int fgs_residual_norm_bwd(const void *dr, int64_t lddr, const void *dn, int64_t lddn,
+                          const void *y, int64_t ldy, const void *r, int64_t ldr, int residual_dtype,
+                          int64_t rows, int64_t width, const float *w_post,
+                          const void *gate, int64_t ldg, int gate_kind, float alpha,
+                          const float *w_pre, float eps,
+                          void *dx, void *dy, void *dgate, float *dw_post, float *dw_pre,
+                          void *workspace, size_t workspace_bytes, void *stream);
+size_t fgs_residual_norm_workspace_bytes(int64_t rows, int64_t width);
+
+/*
+ * fgs_clip_grad_norm -- the global norm of many gradients, and clipping:
+ *   norm = sqrt(sum of the squares of all values), and for every value
+ *   out = g * c with c = max_norm / norm where norm > max_norm, else 1
+ *   (NaN in any gradient makes the norm and every output NaN).
+ * grads    HOST array of `count` entries, read during the call only: data and
+ *          out (DEVICE, may be equal; any alignment of whole values), the
+ *          number of values, and elem FGS_OUT_FP32 or FGS_OUT_BF16.  Tensors
+ *          clipped in place are not written where c is 1.
+ * norm     DEVICE FP32 [1].
+ * Squares are summed in FP64, in a fixed order (no atomics).
+ * workspace  DEVICE scratch, 16-byte aligned, of at least
+ *   fgs_clip_workspace_bytes(count) bytes.
+ */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t count;
+    int64_t elem;
+} fgs_grad;
+int fgs_clip_grad_norm(const fgs_grad *grads, int32_t count, float max_norm, float *norm,
+                       void *workspace, size_t workspace_bytes, void *stream);
+size_t fgs_clip_workspace_bytes(int32_t count);
+
 /* Device workspace needed by TENSOR-mode and NVFP4 quantization (bytes). */
 size_t fgs_workspace_bytes(int64_t rows, int64_t cols);
 
