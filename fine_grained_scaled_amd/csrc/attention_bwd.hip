@@ -31,7 +31,7 @@ struct BwdParams {
     int64_t q_ld, q_hd, k_ld, k_hd, v_ld, v_hd, o_ld, o_hd, do_ld, do_hd;   // elements
     int64_t dq_ld, dq_hd, dk_ld, dk_hd, dv_ld, dv_hd;
     const float* lse;
-    float* ws;            // [H][T] log2 of the row sums, then [H][T] delta
+    float* ws;            // [H][T] -lse / scale, then [H][T] -delta
     const int32_t* cu;
     int64_t T;
     int S, H, Hk, tiles, groups, group_heads, hb;
@@ -100,11 +100,13 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
         for (int j = 0; j < 8; ++j) delta = __builtin_fmaf((float)g[ks][j], (float)o[j], delta);
     }
     delta += swap_half(delta);
-    // a row whose scores are all -Inf has p = 0
-    float lse2 = p.lse[head * p.T + token] * LOG2E;
-    lse2 = lse2 == -__builtin_inff() ? 0.0f : lse2;
+    // the scores start from -lse / scale, so that p = exp2(c s); a row whose
+    // scores are all -Inf has p = 0
+    const float lse = p.lse[head * p.T + token];
+    const float from = lse == -__builtin_inff() ? 0.0f : -lse / p.scale;
+    delta = -delta;
     if (write && half == 0) {
-        p.ws[head * p.T + token] = lse2;
+        p.ws[head * p.T + token] = from;
         p.ws[(p.H + head) * p.T + token] = delta;
     }
 
@@ -132,15 +134,14 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
             if (k0 >= wave_keys) continue;
             f32x16 s, dp;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+            for (int i = 0; i < 16; ++i) s[i] = from, dp[i] = delta;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 s = mfma(read_rows<D>(kt, 32 * t, ks, lane), q[ks], s);
                 dp = mfma(read_rows<D>(vt, 32 * t, ks, lane), g[ks], dp);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
             if (k0 + 31 > w0) {
                 const int seen = min(row, last) - k0 - 4 * half;
 #pragma unroll
@@ -160,17 +161,25 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
     store_row<D>(dq_row, dq, p.scale, lane, write);
 }
 
-// dk and dv: 4 waves of 32 keys, whose key and value rows stay in registers;
-// tiles of 64 query rows and their gradients pass through LDS, head after
-// head of the group.  S = Q K^T and dP = dO V^T leave a lane one key and 16
-// queries a step, again the B operands of dV^T += dO^T P and dK^T += Q^T dS.
+// dk and dv: 8 waves, two sets of 4 that own the same 4 x 32 keys, whose key
+// and value rows stay in registers.  Tiles of 64 query rows and their
+// gradients pass through LDS, head after head of the group, the sets taking
+// turns; at the end the second set hands its sums to the first through LDS.
+// So a workgroup fills a compute unit with two waves a SIMD and the longest
+// of them takes half as long.  S = Q K^T and dP = dO V^T leave a lane one key
+// and 16 queries a step, again the B operands of dV^T += dO^T P and
+// dK^T += Q^T dS; both start from the row's value (-lse / scale, -delta)
+// instead of zero.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attention_dkv_kernel(BwdParams p)
+__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
 {
     constexpr int TILE = QN * D * 2;
-    __shared__ __attribute__((aligned(16))) char lds[4 * TILE + 4 * QN * 4];   // Q0 Q1 dO0 dO1, then the row values
+    constexpr int SET = 4 * TILE + 4 * QN * 4;            // Q0 Q1 dO0 dO1, then the row values
+    __shared__ __attribute__((aligned(16))) char lds_all[2 * SET];
     const int lane = threadIdx.x & 63, half = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+    char* lds = lds_all + set * SET;
     int kv_head, tile;
     {
         const int b = blockIdx.x, G = p.Hk;
@@ -187,8 +196,8 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(BwdParams p)
     if (k0 >= at.len) return;
     const int w0 = k0 + wave * 32;
     const int key = w0 + (lane & 31);
-    const bool write = key < at.len;
-    const int64_t token = at.start + (write ? key : at.len - 1);
+    const bool write = key < at.len && set == 0;
+    const int64_t token = at.start + min(key, at.len - 1);
     uint16_t* dk_row = p.dk + token * p.dk_ld + kv_head * p.dk_hd;
     uint16_t* dv_row = p.dv + token * p.dv_ld + kv_head * p.dv_hd;
 
@@ -228,12 +237,13 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(BwdParams p)
             g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0), 4 * min(lane, last - q0),
                    base + 4 * TILE + (2 * buf + wave) * QN * 4);
     };
-    load(0, 0);
-    for (int n = 0; n < steps; ++n) {
-        const int buf = n & 1;
-        const int q_tile = (q_first + n % q_tiles) * QN;
+    if (set < steps) load(set, 0);
+    for (int m = 0; 2 * m < steps; ++m) {
+        const int buf = m & 1, n = 2 * m + set;
         publish();
-        if (n + 1 < steps) load(n + 1, buf ^ 1);
+        if (n + 2 < steps) load(n + 2, buf ^ 1);
+        if (n >= steps) continue;
+        const int q_tile = (q_first + n % q_tiles) * QN;
         const char* qt = lds + buf * TILE;
         const char* gt = lds + (2 + buf) * TILE;
 #pragma unroll
@@ -241,23 +251,22 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(BwdParams p)
             const int q0 = q_tile + 32 * t;
             if (q0 + 31 < w0 || q0 >= at.len) continue;
             f32x16 s, dp;
+            const float* row_value = values + 2 * buf * QN + 32 * t + 4 * half;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+            for (int i = 0; i < 16; i += 4) {
+                const f32x4 a = *reinterpret_cast<const f32x4*>(row_value + 2 * i);
+                const f32x4 d = *reinterpret_cast<const f32x4*>(row_value + QN + 2 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i + j] = a[j], dp[i + j] = d[j];
+            }
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) s = mfma(read_rows<D>(qt, 32 * t, ks, lane), k[ks], s);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) dp = mfma(read_rows<D>(gt, 32 * t, ks, lane), v[ks], dp);
-            const float* lse2 = values + 2 * buf * QN + 32 * t + 4 * half;
-            const float* delta = lse2 + QN;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const f32x4 a = *reinterpret_cast<const f32x4*>(lse2 + 2 * i);
-                const f32x4 d = *reinterpret_cast<const f32x4*>(delta + 2 * i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + j], c, -a[j]));
-                    dp[i + j] = s[i + j] * (dp[i + j] - d[j]);
-                }
+            for (int i = 0; i < 16; ++i) {
+                s[i] = __builtin_amdgcn_exp2f(s[i] * c);
+                dp[i] *= s[i];
             }
             if (q0 < w0 + 31 || q0 + 32 > at.len) {
                 const int from = key - q0 - 4 * half, to = at.len - q0 - 4 * half;
@@ -276,7 +285,32 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(BwdParams p)
             }
         }
     }
-    if (w0 >= at.len) return;
+    // the second set's sums, 32 keys x D of FP32 a wave, dk and then dv
+    static_assert(4 * 32 * D * 4 <= 2 * SET, "the exchange fits");
+    f32x4* mine = reinterpret_cast<f32x4*>(lds_all) + wave * (32 * D / 4) + lane;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        f32x16* acc = pass ? dv : dk;
+        publish();
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (set)
+                    mine[64 * (4 * dt + g)] = f32x4{acc[dt][4 * g], acc[dt][4 * g + 1], acc[dt][4 * g + 2],
+                                                    acc[dt][4 * g + 3]};
+        publish();
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (!set) {
+                    const f32x4 o = mine[64 * (4 * dt + g)];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[dt][4 * g + j] += o[j];
+                }
+    }
+    if (set || w0 >= at.len) return;
     store_row<D>(dk_row, dk, p.scale, lane, write);
     store_row<D>(dv_row, dv, 1.0f, lane, write);
 }
@@ -303,10 +337,10 @@ hipError_t launch_attention_bwd(const AttentionArgs& a, hipStream_t stream)
     const dim3 grid_kv((unsigned)((a.T / KN + a.S + 2) * a.Hk));
     if (a.D == 128) {
         attention_dq_kernel<128><<<grid, 256, 0, stream>>>(p);
-        attention_dkv_kernel<128><<<grid_kv, 256, 0, stream>>>(p);
+        attention_dkv_kernel<128><<<grid_kv, 512, 0, stream>>>(p);
     } else {
         attention_dq_kernel<64><<<grid, 256, 0, stream>>>(p);
-        attention_dkv_kernel<64><<<grid_kv, 256, 0, stream>>>(p);
+        attention_dkv_kernel<64><<<grid_kv, 512, 0, stream>>>(p);
     }
     return hipGetLastError();
 }
