@@ -39,7 +39,7 @@ struct BwdParams {
 };
 
 constexpr int BN = 64;    // keys a tile of the dq kernel
-constexpr int QN = 64;    // query rows a tile of the dk, dv kernel
+constexpr int QN = 32;    // query rows a tile of the dk, dv kernel
 constexpr int KN = 128;   // keys a workgroup of it
 
 // dq: 4 waves as in the forward kernel (HB heads x 128 / HB tokens, 32 rows a
@@ -162,7 +162,8 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
 }
 
 // dk and dv: 8 waves, two sets of 4 that own the same 4 x 32 keys, whose key
-// and value rows stay in registers.  Tiles of 64 query rows and their
+// rows stay in registers, and whose value rows do as far as 256 registers
+// reach (the other half lies in LDS).  Tiles of 64 query rows and their
 // gradients pass through LDS, head after head of the group, the sets taking
 // turns; at the end the second set hands its sums to the first through LDS.
 // So a workgroup fills a compute unit with two waves a SIMD and the longest
@@ -174,8 +175,9 @@ template <int D>
 __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
 {
     constexpr int TILE = QN * D * 2;
-    constexpr int SET = 4 * TILE + 4 * QN * 4;            // Q0 Q1 dO0 dO1, then the row values
-    __shared__ __attribute__((aligned(16))) char lds_all[2 * SET];
+    constexpr int SET = 4 * TILE + 4 * 64 * 4;            // Q0 Q1 dO0 dO1, then the row values, 64 a copy
+    constexpr int KEYS = KN * D * 2;
+    __shared__ __attribute__((aligned(16))) char lds_all[2 * SET + 2 * KEYS];
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
@@ -211,58 +213,64 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
         store_row<D>(dv_row, dv, 0.0f, lane, write);
         return;
     }
-    const uint16_t* k_row = p.k + token * p.k_ld + kv_head * p.k_hd;
-    const uint16_t* v_row = p.v + token * p.v_ld + kv_head * p.v_hd;
-    bf16x8 k[D / 16], v[D / 16];
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-        k[ks] = *reinterpret_cast<const bf16x8*>(k_row + 16 * ks + 8 * half);
-        v[ks] = *reinterpret_cast<const bf16x8*>(v_row + 16 * ks + 8 * half);
-    }
-
     const uint32_t base = lds_offset(lds);
     const float* values = reinterpret_cast<const float*>(lds + 4 * TILE);
     const int last = at.len - 1;
     const int q_first = k0 / QN, q_tiles = (at.len + QN - 1) / QN - q_first;
     const int steps = q_tiles * p.group_heads;
     const float c = p.scale * LOG2E;
-    auto load = [&](int n, int buf) {
-        const int head = kv_head * p.group_heads + n / q_tiles;
-        const int q0 = (q_first + n % q_tiles) * QN;
+    const char* kt = lds_all + 2 * SET;
+    const char* vt = kt + KEYS;
+    stage<D, KN, 8>(uniform_ptr(p.k + (at.start + k0) * p.k_ld + kv_head * p.k_hd), (uint32_t)p.k_ld * 2, last - k0,
+                    lds_offset(kt), 4 * set + wave, lane);
+    stage<D, KN, 8>(uniform_ptr(p.v + (at.start + k0) * p.v_ld + kv_head * p.v_hd), (uint32_t)p.v_ld * 2, last - k0,
+                    lds_offset(vt), 4 * set + wave, lane);
+    // the set's step, its head and query tile, and those of the step it loads
+    int head = kv_head * p.group_heads, q_index = set, next_head, next_index;
+    auto forward = [&](int& h, int& i) {
+        while (i >= q_tiles) i -= q_tiles, ++h;
+    };
+    forward(head, q_index);
+    auto load = [&](int head, int q_index, int buf) {
+        const int q0 = (q_first + q_index) * QN;
         const uint16_t* q = uniform_ptr(p.q + (at.start + q0) * p.q_ld + head * p.q_hd);
         const uint16_t* g = uniform_ptr(p.dout + (at.start + q0) * p.do_ld + head * p.do_hd);
         stage<D, QN, 4>(q, (uint32_t)p.q_ld * 2, last - q0, base + buf * TILE, wave, lane);
         stage<D, QN, 4>(g, (uint32_t)p.do_ld * 2, last - q0, base + (2 + buf) * TILE, wave, lane);
         if (wave < 2)
-            g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0), 4 * min(lane, last - q0),
-                   base + 4 * TILE + (2 * buf + wave) * QN * 4);
+            g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0), 4 * min(lane & (QN - 1), last - q0),
+                   base + 4 * TILE + (2 * buf + wave) * 256);
     };
-    if (set < steps) load(set, 0);
+    if (set < steps) load(head, q_index, 0);
     for (int m = 0; 2 * m < steps; ++m) {
         const int buf = m & 1, n = 2 * m + set;
         publish();
-        if (n + 2 < steps) load(n + 2, buf ^ 1);
         if (n >= steps) continue;
-        const int q_tile = (q_first + n % q_tiles) * QN;
+        next_head = head, next_index = q_index + 2;
+        forward(next_head, next_index);
+        if (n + 2 < steps) load(next_head, next_index, buf ^ 1);
+        const int q_tile = (q_first + q_index) * QN;
+        head = next_head, q_index = next_index;
         const char* qt = lds + buf * TILE;
         const char* gt = lds + (2 + buf) * TILE;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < QN / 32; ++t) {
             const int q0 = q_tile + 32 * t;
             if (q0 + 31 < w0 || q0 >= at.len) continue;
             f32x16 s, dp;
-            const float* row_value = values + 2 * buf * QN + 32 * t + 4 * half;
+            const float* row_value = values + 2 * buf * 64 + 32 * t + 4 * half;
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const f32x4 a = *reinterpret_cast<const f32x4*>(row_value + 2 * i);
-                const f32x4 d = *reinterpret_cast<const f32x4*>(row_value + QN + 2 * i);
+                const f32x4 d = *reinterpret_cast<const f32x4*>(row_value + 64 + 2 * i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i + j] = a[j], dp[i + j] = d[j];
             }
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) s = mfma(read_rows<D>(qt, 32 * t, ks, lane), k[ks], s);
+            for (int ks = 0; ks < D / 16; ++ks) s = mfma(read_rows<D>(qt, 32 * t, ks, lane), read_rows<D>(kt, 32 * wave, ks, lane), s);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) dp = mfma(read_rows<D>(gt, 32 * t, ks, lane), v[ks], dp);
+            for (int ks = 0; ks < D / 16; ++ks)
+                dp = mfma(read_rows<D>(gt, 32 * t, ks, lane), read_rows<D>(vt, 32 * wave, ks, lane), dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[i] = __builtin_amdgcn_exp2f(s[i] * c);
