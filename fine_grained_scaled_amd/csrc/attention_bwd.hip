@@ -34,7 +34,7 @@ struct BwdParams {
     float* ws;            // [H][T] -lse / scale, then [H][T] -delta
     const int32_t* cu;
     int64_t T;
-    int S, H, Hk, tiles, groups, group_heads, hb;
+    int S, H, Hk, tiles, kv_tiles, groups, group_heads, hb;
     float scale;
 };
 
@@ -51,20 +51,10 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
     __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int group, tile;
-    {
-        const int b = blockIdx.x, G = p.groups;
-        if (G % 8 == 0) {
-            group = (b & 7) * (G / 8) + (b >> 3) % (G / 8);
-            tile = (b >> 3) / (G / 8);
-        } else {
-            group = b % G;
-            tile = b / G;
-        }
-        tile = p.tiles - 1 - tile;
-    }
     const int rows = 128 / p.hb;
-    const Where at = find_tile(p.cu, p.S, p.T, rows, tile, lane);
+    const Mine mine = my_tile<false>(p.cu, p.S, p.T, rows, p.tiles, p.groups, lane);
+    const Where at = mine.at;
+    const int group = mine.group;
     const int t0 = at.tile * rows;
     if (t0 >= at.len) return;
     const int head = group * p.hb + wave % p.hb;
@@ -122,6 +112,7 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
                         lane);
     };
     load(0, 0);
+    registers_landed();
     for (int n = 0; n < n_tiles; ++n) {
         const int buf = n & 1;
         publish();
@@ -182,18 +173,9 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     const int set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
     char* lds = lds_all + set * SET;
-    int kv_head, tile;
-    {
-        const int b = blockIdx.x, G = p.Hk;
-        if (G % 8 == 0) {
-            kv_head = (b & 7) * (G / 8) + (b >> 3) % (G / 8);
-            tile = (b >> 3) / (G / 8);
-        } else {
-            kv_head = b % G;
-            tile = b / G;
-        }
-    }
-    const Where at = find_tile(p.cu, p.S, p.T, KN, tile, lane);
+    const Mine mine = my_tile<true>(p.cu, p.S, p.T, KN, p.kv_tiles, p.Hk, lane);
+    const Where at = mine.at;
+    const int kv_head = mine.group;
     const int k0 = at.tile * KN;
     if (k0 >= at.len) return;
     const int w0 = k0 + wave * 32;
@@ -295,7 +277,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     }
     // the second set's sums, 32 keys x D of FP32 a wave, dk and then dv
     static_assert(4 * 32 * D * 4 <= 2 * SET, "the exchange fits");
-    f32x4* mine = reinterpret_cast<f32x4*>(lds_all) + wave * (32 * D / 4) + lane;
+    f32x4* swap = reinterpret_cast<f32x4*>(lds_all) + wave * (32 * D / 4) + lane;
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
         f32x16* acc = pass ? dv : dk;
@@ -305,7 +287,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 if (set)
-                    mine[64 * (4 * dt + g)] = f32x4{acc[dt][4 * g], acc[dt][4 * g + 1], acc[dt][4 * g + 2],
+                    swap[64 * (4 * dt + g)] = f32x4{acc[dt][4 * g], acc[dt][4 * g + 1], acc[dt][4 * g + 2],
                                                     acc[dt][4 * g + 3]};
         publish();
 #pragma unroll
@@ -313,7 +295,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 if (!set) {
-                    const f32x4 o = mine[64 * (4 * dt + g)];
+                    const f32x4 o = swap[64 * (4 * dt + g)];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[dt][4 * g + j] += o[j];
                 }
@@ -342,7 +324,8 @@ hipError_t launch_attention_bwd(const AttentionArgs& a, hipStream_t stream)
     p.tiles = (int)(a.T / (128 / p.hb)) + a.S + 2;
     p.scale = a.scale;
     const dim3 grid((unsigned)((int64_t)p.tiles * p.groups));
-    const dim3 grid_kv((unsigned)((a.T / KN + a.S + 2) * a.Hk));
+    p.kv_tiles = (int)(a.T / KN) + a.S + 2;
+    const dim3 grid_kv((unsigned)((int64_t)p.kv_tiles * a.Hk));
     if (a.D == 128) {
         attention_dq_kernel<128><<<grid, 256, 0, stream>>>(p);
         attention_dkv_kernel<128><<<grid_kv, 512, 0, stream>>>(p);

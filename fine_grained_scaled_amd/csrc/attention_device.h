@@ -92,6 +92,11 @@ __device__ __forceinline__ void publish()
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// Every load into registers so far has landed, in a form that the compiler
+// sees: before a loop that issues copies, or its waits for those registers
+// inside the loop would wait for the copies as well.
+__device__ __forceinline__ void registers_landed() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0)
+
 // ROWS rows at `base` (uniform; row stride ld bytes, below 2^24) into LDS at
 // `lds`, split over the workgroup's WAVES waves.  Rows past `last` repeat row
 // `last`, so nothing outside the sequence is read.
@@ -198,6 +203,91 @@ __device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, 
     w.len = __builtin_amdgcn_readfirstlane(b > a && w.tile >= 0 ? (int)(b - a) : 0);
     w.sequence = seg > 0 && seg <= S;
     return w;
+}
+
+// The same tiles by the work they stand for, most first: a tile that is the
+// m-th of its segment counted from the cheap end (the first query tile sees
+// the fewest keys, the last key tile is seen by the fewest queries) has size
+// m, and workgroup `rank` takes the rank-th tile in order of falling size, so
+// that the longest workgroups start first and the shortest fill the end.
+// Up to SORTED - 2 sequences; each lane holds a few segments.
+constexpr int SORTED = 256;
+template <bool KEYS>
+__device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int64_t T, int rows, int rank, int lane)
+{
+    constexpr int C = SORTED / 64;
+    int n[C], most = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const int i = 64 * j + lane;
+        n[j] = 0;
+        if (64 * j < S + 2 && i < S + 2) {
+            const int64_t len = segment_start(cu, S, T, i + 1) - segment_start(cu, S, T, i);
+            n[j] = len > 0 ? (int)((len + rows - 1) / rows) : 0;
+            most = max(most, n[j]);
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) most = max(most, __shfl_xor(most, m));
+    most = __builtin_amdgcn_readfirstlane(most);
+    auto larger = [&](int m) {          // tiles of a size above m
+        int v = 0;
+#pragma unroll
+        for (int j = 0; j < C; ++j) v += max(n[j] - m, 0);
+#pragma unroll
+        for (int k = 1; k < 64; k *= 2) v += __shfl_xor(v, k);
+        return __builtin_amdgcn_readfirstlane(v);
+    };
+    Where w{0, 0, 0, false};
+    if (rank >= larger(0)) return w;
+    int lo = 1, hi = most;              // the smallest m with at most `rank` larger tiles
+    while (lo < hi) {
+        const int m = (lo + hi) / 2;
+        if (larger(m) <= rank) hi = m;
+        else lo = m + 1;
+    }
+    int r = rank - larger(lo), seg = 0, tiles = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {       // the r-th segment that has a tile of this size
+        const uint64_t has = __ballot(n[j] >= lo);
+        const int c = __popcll(has), before = __popcll(has & ((1ull << lane) - 1));
+        const uint64_t hit = __ballot(n[j] >= lo && before == r);
+        if (r >= 0 && r < c) {
+            const int at = __ffsll((unsigned long long)hit) - 1;
+            seg = 64 * j + at;
+            tiles = __builtin_amdgcn_readlane(n[j], at);
+        }
+        r -= c;
+    }
+    seg = __builtin_amdgcn_readfirstlane(seg);
+    const int64_t a = segment_start(cu, S, T, seg), b = segment_start(cu, S, T, seg + 1);
+    w.start = __builtin_amdgcn_readfirstlane((int)a);
+    w.len = __builtin_amdgcn_readfirstlane((int)(b - a));
+    w.tile = __builtin_amdgcn_readfirstlane(KEYS ? tiles - lo : lo - 1);
+    w.sequence = seg > 0 && seg <= S;
+    return w;
+}
+
+// Workgroup b of a grid of `tiles` x `groups`: its tile and its group of
+// heads.  Workgroups go round the 8 XCDs, each with its own L2: with a
+// multiple of 8 groups, one XCD keeps the same heads.
+struct Mine { Where at; int group; };
+template <bool KEYS>
+__device__ __forceinline__ Mine my_tile(const int32_t* cu, int S, int64_t T, int rows, int tiles, int groups, int lane)
+{
+    const int b = blockIdx.x;
+    Mine m;
+    int rank;
+    if (groups % 8 == 0) {
+        m.group = (b & 7) * (groups / 8) + (b >> 3) % (groups / 8);
+        rank = (b >> 3) / (groups / 8);
+    } else {
+        m.group = b % groups;
+        rank = b / groups;
+    }
+    if (KEYS && S + 2 <= SORTED) m.at = find_tile_by_size<KEYS>(cu, S, T, rows, rank, lane);
+    else m.at = find_tile(cu, S, T, rows, KEYS ? rank : tiles - 1 - rank, lane);
+    return m;
 }
 
 } // namespace attn

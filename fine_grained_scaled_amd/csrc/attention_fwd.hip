@@ -95,23 +95,10 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    // Workgroups go round the 8 XCDs, each with its own L2: with a multiple
-    // of 8 of them a token tile, one XCD keeps the same key heads.  The last
-    // tiles, which see the most keys, go first.
-    int group, tile;
-    {
-        const int b = blockIdx.x, G = p.groups;
-        if (G % 8 == 0) {
-            group = (b & 7) * (G / 8) + (b >> 3) % (G / 8);
-            tile = (b >> 3) / (G / 8);
-        } else {
-            group = b % G;
-            tile = b / G;
-        }
-        tile = p.tiles - 1 - tile;
-    }
     const int rows = 128 / p.hb;
-    const Where at = find_tile(p.cu, p.S, p.T, rows, tile, lane);
+    const Mine mine = my_tile<false>(p.cu, p.S, p.T, rows, p.tiles, p.groups, lane);
+    const Where at = mine.at;
+    const int group = mine.group;
     const int t0 = at.tile * rows;
     if (t0 >= at.len) return;
     const int head = group * p.hb + wave % p.hb;
@@ -155,6 +142,7 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
                         lane);
     };
     load(0, 0);
+    registers_landed();
     for (int n = 0; n < n_tiles; ++n) {
         const int buf = n & 1, k0 = n * BN;
         publish();

@@ -39,7 +39,7 @@ def _check(lengths, H, Hk, D, scale=None, **how):
 
 # lengths around the tiles of 32, 64 and 128 rows, and sequences of none
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("lengths", [[1], [2, 1, 0, 3], [31, 33], [64], [65, 63], [127, 0, 128, 129], [300], [17] * 70],
+@pytest.mark.parametrize("lengths", [[1], [2, 1, 0, 3], [31, 33], [64], [65, 63], [127, 0, 128, 129], [300], [17] * 70, [3] * 254, [2] * 255],
                          ids=str)
 def test_lengths(lengths, D):
     _check(lengths, 4, 2, D, seed=len(lengths))
