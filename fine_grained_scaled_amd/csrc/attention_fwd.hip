@@ -17,6 +17,8 @@
 // S^T = K Q^T, so a lane holds 32 keys of one query: its maximum and sum need
 // one exchange between lane halves, and its probabilities are already the B
 // operand of O^T = V^T P^T (attention_device.h).
+#include <type_traits>
+
 #include "attention_device.h"
 
 namespace fgs {
@@ -133,77 +135,151 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
     const int n_tiles = (min(t0 + rows, at.len) + BN - 1) / BN;
     const int wave_keys = w0 < at.len ? min(w0 + 32, at.len) : 0;     // keys that some row of the wave sees
     const float c = p.scale * LOG2E;
-    float m = -__builtin_inff(), l = 0.0f;             // maximum of the raw scores; the lane half's sum
+    float m = 0.0f, l = 0.0f;                          // what the exponents are taken from; the lane half's sum
+    const int wave_tiles = (wave_keys + BN - 1) / BN;
 
-    auto load = [&](int n, int buf) {
-        const int k0 = n * BN;
-        stage<D, BN, 4>(k_seq + (int64_t)k0 * p.k_ld, (uint32_t)p.k_ld * 2, last - k0, base + buf * TILE, wave, lane);
-        stage<D, BN, 4>(v_seq + (int64_t)k0 * p.v_ld, (uint32_t)p.v_ld * 2, last - k0, base + (2 + buf) * TILE, wave,
-                        lane);
+    auto load_k = [&](int n) {
+        stage<D, BN, 4>(k_seq + (int64_t)n * BN * p.k_ld, (uint32_t)p.k_ld * 2, last - n * BN, base + (n & 1) * TILE,
+                        wave, lane);
     };
-    load(0, 0);
-    registers_landed();
-    for (int n = 0; n < n_tiles; ++n) {
-        const int buf = n & 1, k0 = n * BN;
-        publish();
-        if (n + 1 < n_tiles) load(n + 1, buf ^ 1);
-        if (k0 >= wave_keys) continue;
-        const char* kt = lds + buf * TILE;
-        const char* vt = lds + (2 + buf) * TILE;
-
-        f32x16 s[2];
+    auto load_v = [&](int n) {
+        stage<D, BN, 4>(v_seq + (int64_t)n * BN * p.v_ld, (uint32_t)p.v_ld * 2, last - n * BN,
+                        base + (2 + (n & 1)) * TILE, wave, lane);
+    };
+    // The scores of a tile, and in between the exponents of `old` (with
+    // exponents_too): one 16-deep step of both key halves, then the exponents
+    // of as many registers, so that the vector unit works while the matrix
+    // unit does; operands are read two steps ahead.  The compiler keeps
+    // this order (the barriers to its scheduler), left to itself it reads
+    // each operand right before its use.
+    constexpr int KS = D / 16, CHUNK = 32 / KS;
+    auto exponent_pair = [&](const f32x16 (&s)[2], int i, float mc, float (&sum)[2], uint32_t (&pr)[16]) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16], c, -mc));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16 + 1], c, -mc));
+        sum[0] += e0, sum[1] += e1;
+        const bf16x2 w = {(__bf16)e0, (__bf16)e1};
+        pr[i / 2] = __builtin_bit_cast(uint32_t, w);
+    };
+    auto scores = [&](auto exponents_too, int n, f32x16 (&s)[2], const f32x16 (&old)[2],
+                      uint32_t (&pr)[16]) {
+        const char* kt = lds + (n & 1) * TILE;
+        const float mc = m * c;
+        float sum[2] = {0.0f, 0.0f};
+        bf16x8 k[KS][2];
+        auto read = [&](int ks) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < 2; ++t) k[ks][t] = read_rows<D>(kt, 32 * t, ks, lane);
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+        read(0);
+        read(1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) s[t] = mfma(read_rows<D>(kt, 32 * t, ks, lane), q[ks], s[t]);
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 2 < KS) read(ks + 2);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[t] = mfma(k[ks][t], q[ks], s[t]);
+            if constexpr (decltype(exponents_too)::value)
+#pragma unroll
+                for (int i = ks * CHUNK; i < (ks + 1) * CHUNK; i += 2) {
+                    exponent_pair(old, i, mc, sum, pr);
+                    // here, and not together with the other branch's
+                    asm volatile("" : "+v"(pr[i / 2]), "+v"(sum[0]), "+v"(sum[1]));
+                }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (k0 + BN > w0) {                            // the diagonal: hide the keys after the row
-            const int seen = min(row, last) - k0 - 4 * half;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (32 * t + acc_row(i, 0) > seen) s[t][i] = -__builtin_inff();
-        }
+        return sum[0] + sum[1];
+    };
+    auto row_top = [&](const f32x16 (&s)[2]) {
         float top = s[0][0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[1][i]);
-        top = fmaxf(top, swap_half(top));
-        // The maximum only has to keep exp2 in range: it moves when a score
-        // passes it by more than a factor of 2^8, so most tiles leave the
-        // output accumulators as they are.
-        if (__any((top - m) * c > 8.0f)) {
-            const float next = fmaxf(m, top);
-            const float safe = next == -__builtin_inff() ? 0.0f : next;
-            const float old = __builtin_amdgcn_exp2f((m - safe) * c);
-            m = next;
+        return fmaxf(top, swap_half(top));
+    };
+    auto hide = [&](int n, f32x16 (&s)[2]) {           // the diagonal: the keys after the row
+        const int k0 = n * BN;
+        if (k0 + BN <= w0) return;
+        const int seen = min(row, last) - k0 - 4 * half;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (32 * t + acc_row(i, 0) > seen) s[t][i] = -__builtin_inff();
+    };
+    auto exponents = [&](const f32x16 (&s)[2], uint32_t (&pr)[16]) {
+        const float mc = m * c;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) exponent_pair(s, i, mc, sum, pr);
+        return sum[0] + sum[1];
+    };
+    // One tile: its exponents while the matrix unit forms the next tile's
+    // scores, then its values' product.
+    auto step = [&](int n, f32x16 (&s)[2], f32x16 (&next)[2]) {
+        publish();
+        if (n + 2 < n_tiles) load_k(n + 2);
+        if (n + 1 < n_tiles) load_v(n + 1);
+        if (n >= wave_tiles) return;
+        hide(n, s);
+        if (n == 0) {
+            const float top = row_top(s);
+            m = top == -__builtin_inff() ? 0.0f : top;
+        }
+        uint32_t pr[16];
+        float sum;
+        if (n + 1 < wave_tiles) sum = scores(std::true_type{}, n + 1, next, s, pr);
+        else sum = exponents(s, pr);
+        // m only has to keep exp2 in range: it moves when a row's exponents
+        // pass 2^14, or when nothing of the row is above 2^-60 yet, so most
+        // tiles never look for their maximum nor touch the output sums.
+        if (__any(!(sum <= 16384.0f) || (l == 0.0f && sum < 0x1p-60f))) {
+            const float top = row_top(s);
+            const bool none = l + swap_half(l) == 0.0f;
+            const float to = none ? (top == -__builtin_inff() ? m : top) : fmaxf(m, top);
+            const float old = none ? 1.0f : __builtin_amdgcn_exp2f((m - to) * c);
+            m = to;
             l *= old;
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[dt][i] *= old;
+            sum = exponents(s, pr);
         }
-        const float mc = m == -__builtin_inff() ? 0.0f : m * c;
+        l += sum;
+        // operands are read three products ahead, as above
+        constexpr int F = 4 * (D / 32);
+        const char* vt = lds + (2 + (n & 1)) * TILE;
+        bf16x8 v[F];
+        auto read = [&](int f) { v[f] = read_tr<D>(vt, 16 * (f / (D / 32)), f % (D / 32), lane); };
+        read(0);
+        read(1);
+        read(2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -mc));
-                l += s[t][i];
-            }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bf16x8 pr = pack8(s[t], 8 * ks);
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt)
-                    o[dt] = mfma(read_tr<D>(vt, 32 * t + 16 * ks, dt, lane), pr, o[dt]);
-            }
+        for (int f = 0; f < F; ++f) {
+            if (f + 3 < F) read(f + 3);
+            const int w = f / (D / 32) * 4;
+            const u32x4 b = {pr[w], pr[w + 1], pr[w + 2], pr[w + 3]};
+            o[f % (D / 32)] = mfma(v[f], __builtin_bit_cast(bf16x8, b), o[f % (D / 32)]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    load_k(0);
+    load_v(0);
+    if (n_tiles > 1) load_k(1);
+    registers_landed();
+    publish();
+    f32x16 sa[2], sb[2];
+    uint32_t unused[16];
+    if (wave_tiles > 0) scores(std::false_type{}, 0, sa, sb, unused);
+    for (int n = 0; n < n_tiles; n += 2) {
+        step(n, sa, sb);
+        if (n + 1 < n_tiles) step(n + 1, sb, sa);
     }
     if (w0 >= at.len) return;
     l += swap_half(l);
