@@ -39,7 +39,7 @@ struct BwdParams {
 };
 
 constexpr int BN = 64;    // keys a tile of the dq kernel
-constexpr int QN = 32;    // query rows a tile of the dk, dv kernel
+constexpr int QN = 64;    // query rows a tile of the dk, dv kernel
 constexpr int KN = 128;   // keys a workgroup of it
 
 // dq: 4 waves as in the forward kernel (HB heads x 128 / HB tokens, 32 rows a
@@ -166,13 +166,12 @@ template <int D>
 __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
 {
     constexpr int TILE = QN * D * 2;
-    constexpr int SET = 4 * TILE + 4 * 64 * 4;            // Q0 Q1 dO0 dO1, then the row values, 64 a copy
-    constexpr int KEYS = KN * D * 2;
-    __shared__ __attribute__((aligned(16))) char lds_all[2 * SET + 2 * KEYS];
+    constexpr int STAGE = 2 * TILE + 2 * 64 * 4;          // Q, dO, then the row values, 64 a copy
+    __shared__ __attribute__((aligned(256))) char lds_all[4 * STAGE];
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
-    char* lds = lds_all + set * SET;
+    char* lds = lds_all + set * 2 * STAGE;
     const Mine mine = my_tile<true>(p.cu, p.S, p.T, KN, p.kv_tiles, p.Hk, lane);
     const Where at = mine.at;
     const int kv_head = mine.group;
@@ -181,102 +180,139 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     const int w0 = k0 + wave * 32;
     const int key = w0 + (lane & 31);
     const bool write = key < at.len && set == 0;
-    const int64_t token = at.start + min(key, at.len - 1);
-    uint16_t* dk_row = p.dk + token * p.dk_ld + kv_head * p.dk_hd;
-    uint16_t* dv_row = p.dv + token * p.dv_ld + kv_head * p.dv_hd;
+    auto token_of = [&](int key) { return at.start + min(key, at.len - 1); };
 
     f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
-    if (!at.sequence) {
-        store_row<D>(dk_row, dk, 0.0f, lane, write);
-        store_row<D>(dv_row, dv, 0.0f, lane, write);
-        return;
+    auto store = [&] {
+        int key_now = key;                     // addresses formed here are not kept in registers until the end
+        asm volatile("" : "+v"(key_now));
+        const int64_t token = token_of(key_now);
+        store_row<D>(p.dk + token * p.dk_ld + kv_head * p.dk_hd, dk, p.scale, lane, write);
+        store_row<D>(p.dv + token * p.dv_ld + kv_head * p.dv_hd, dv, 1.0f, lane, write);
+    };
+    if (!at.sequence) return store();
+    const int64_t token = token_of(key);
+    const uint16_t* k_row = p.k + token * p.k_ld + kv_head * p.k_hd;
+    const uint16_t* v_row = p.v + token * p.v_ld + kv_head * p.v_hd;
+    bf16x8 k[D / 16], v[D / 16];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        k[ks] = *reinterpret_cast<const bf16x8*>(k_row + 16 * ks + 8 * half);
+        v[ks] = *reinterpret_cast<const bf16x8*>(v_row + 16 * ks + 8 * half);
     }
     const uint32_t base = lds_offset(lds);
-    const float* values = reinterpret_cast<const float*>(lds + 4 * TILE);
     const int last = at.len - 1;
     const int q_first = k0 / QN, q_tiles = (at.len + QN - 1) / QN - q_first;
     const int steps = q_tiles * p.group_heads;
     const float c = p.scale * LOG2E;
-    const char* kt = lds_all + 2 * SET;
-    const char* vt = kt + KEYS;
-    stage<D, KN, 8>(uniform_ptr(p.k + (at.start + k0) * p.k_ld + kv_head * p.k_hd), (uint32_t)p.k_ld * 2, last - k0,
-                    lds_offset(kt), 4 * set + wave, lane);
-    stage<D, KN, 8>(uniform_ptr(p.v + (at.start + k0) * p.v_ld + kv_head * p.v_hd), (uint32_t)p.v_ld * 2, last - k0,
-                    lds_offset(vt), 4 * set + wave, lane);
-    // the set's step, its head and query tile, and those of the step it loads
-    int head = kv_head * p.group_heads, q_index = set, next_head, next_index;
+    // the head and the query tile of the set's step
+    int head = kv_head * p.group_heads, q_index = set;
     auto forward = [&](int& h, int& i) {
         while (i >= q_tiles) i -= q_tiles, ++h;
     };
     forward(head, q_index);
-    auto load = [&](int head, int q_index, int buf) {
+    auto load = [&](int head, int q_index, int stage_at) {
         const int q0 = (q_first + q_index) * QN;
         const uint16_t* q = uniform_ptr(p.q + (at.start + q0) * p.q_ld + head * p.q_hd);
         const uint16_t* g = uniform_ptr(p.dout + (at.start + q0) * p.do_ld + head * p.do_hd);
-        stage<D, QN, 4>(q, (uint32_t)p.q_ld * 2, last - q0, base + buf * TILE, wave, lane);
-        stage<D, QN, 4>(g, (uint32_t)p.do_ld * 2, last - q0, base + (2 + buf) * TILE, wave, lane);
+        const uint32_t to = base + stage_at * STAGE;
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));         // nothing of the copies' addresses stays in registers between them
+        stage<D, QN, 4>(q, (uint32_t)p.q_ld * 2, last - q0, to, wave, lane);
+        stage<D, QN, 4>(g, (uint32_t)p.do_ld * 2, last - q0, to + TILE, wave, lane);
         if (wave < 2)
-            g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0), 4 * min(lane & (QN - 1), last - q0),
-                   base + 4 * TILE + (2 * buf + wave) * 256);
+            g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0),
+                   4 * min(lane & (QN - 1), last - q0), to + 2 * TILE + wave * 256);
     };
-    if (set < steps) load(head, q_index, 0);
-    for (int m = 0; 2 * m < steps; ++m) {
-        const int buf = m & 1, n = 2 * m + set;
-        publish();
-        if (n >= steps) continue;
-        next_head = head, next_index = q_index + 2;
-        forward(next_head, next_index);
-        if (n + 2 < steps) load(next_head, next_index, buf ^ 1);
-        const int q_tile = (q_first + q_index) * QN;
-        head = next_head, q_index = next_index;
-        const char* qt = lds + buf * TILE;
-        const char* gt = lds + (2 + buf) * TILE;
+    // 32 queries and the wave's 32 keys.  256 registers hold the sums, the
+    // keys and values and two score tiles with little to spare: operands are
+    // read two products ahead, which the scheduler barriers keep in place.
+    const uint32_t rows_at = rows_address<D>(lane), tr_at = tr_address<D>(lane);
+    auto step = [&](uint32_t tile, const float* row_value, int q0) {
+        f32x16 s, dp;
 #pragma unroll
-        for (int t = 0; t < QN / 32; ++t) {
-            const int q0 = q_tile + 32 * t;
-            if (q0 + 31 < w0 || q0 >= at.len) continue;
-            f32x16 s, dp;
-            const float* row_value = values + 2 * buf * 64 + 32 * t + 4 * half;
+        for (int i = 0; i < 16; i += 4) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(row_value + 2 * i);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const f32x4 a = *reinterpret_cast<const f32x4*>(row_value + 2 * i);
-                const f32x4 d = *reinterpret_cast<const f32x4*>(row_value + 64 + 2 * i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i + j] = a[j], dp[i + j] = d[j];
-            }
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) s = mfma(read_rows<D>(qt, 32 * t, ks, lane), read_rows<D>(kt, 32 * wave, ks, lane), s);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                dp = mfma(read_rows<D>(gt, 32 * t, ks, lane), read_rows<D>(vt, 32 * wave, ks, lane), dp);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[i] = __builtin_amdgcn_exp2f(s[i] * c);
-                dp[i] *= s[i];
-            }
-            if (q0 < w0 + 31 || q0 + 32 > at.len) {
-                const int from = key - q0 - 4 * half, to = at.len - q0 - 4 * half;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (acc_row(i, 0) < from || acc_row(i, 0) >= to) s[i] = dp[i] = 0.0f;
-            }
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bf16x8 pr = pack8(s, 8 * ks), ds = pack8(dp, 8 * ks);
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) {
-                    dv[dt] = mfma(read_tr<D>(gt, 32 * t + 16 * ks, dt, lane), pr, dv[dt]);
-                    dk[dt] = mfma(read_tr<D>(qt, 32 * t + 16 * ks, dt, lane), ds, dk[dt]);
-                }
-            }
+            for (int j = 0; j < 4; ++j) s[i + j] = a[j];
         }
+        constexpr int KS = D / 16;
+        bf16x8 x[2 * KS];
+        uint32_t at_row = tile + rows_at;
+        asm volatile("" : "+v"(at_row));
+        auto read = [&](int f) { x[f] = read_rows_at(at_row, f % KS, f < KS ? 0 : TILE); };
+        read(0);
+        read(1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < 2 * KS; ++f) {
+            if (f + 2 < 2 * KS) read(f + 2);
+            if (f == KS - 4)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const f32x4 d = *reinterpret_cast<const f32x4*>(row_value + 64 + 2 * i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dp[i + j] = d[j];
+                }
+            if (f < KS) s = mfma(x[f], k[f], s);
+            else dp = mfma(x[f], v[f - KS], dp);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        constexpr int DT = D / 32, F = 4 * DT;
+        bf16x8 y[F];
+        uint32_t at_tr = tile + tr_at;
+        asm volatile("" : "+v"(at_tr));
+        auto read2 = [&](int f) {       // of dv, then of dk: rows 16 (f / DT % 2), columns 32 (f % DT)
+            y[f] = read_tr_at<D>(at_tr, 16 * (f / DT % 2), f % DT, f < 2 * DT ? TILE : 0);
+        };
+        read2(0);
+        read2(1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(s[i] * c);
+            dp[i] *= s[i];
+        }
+        if (q0 < w0 + 31 || q0 + 32 > at.len) {
+            const int from = key - q0 - 4 * half, to = at.len - q0 - 4 * half;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (acc_row(i, 0) < from || acc_row(i, 0) >= to) s[i] = dp[i] = 0.0f;
+        }
+        bf16x8 pr[2], ds[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) pr[ks] = pack8(s, 8 * ks), ds[ks] = pack8(dp, 8 * ks);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            if (f + 2 < F) read2(f + 2);
+            if (f < 2 * DT) dv[f % DT] = mfma(y[f], pr[f / DT], dv[f % DT]);
+            else dk[f % DT] = mfma(y[f], ds[f / DT - 2], dk[f % DT]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const int set_steps = (steps + 1 - set) / 2, all_steps = (steps + 1) / 2;
+    if (set_steps > 0) load(head, q_index, 0);
+    registers_landed();
+    for (int m = 0; m < all_steps; ++m) {
+        publish();
+        const int q0 = (q_first + q_index) * QN;
+        q_index += 2;
+        forward(head, q_index);
+        if (m + 1 < set_steps) load(head, q_index, (m + 1) & 1);
+        if (m >= set_steps) continue;
+        const uint32_t tile = base + (m & 1) * STAGE;
+        const float* row_value = reinterpret_cast<const float*>(lds + (m & 1) * STAGE + 2 * TILE) + 4 * half;
+#pragma unroll
+        for (int t = 0; t < QN / 32; ++t)
+            if (q0 + 32 * t + 31 >= w0 && q0 + 32 * t < at.len)
+                step(tile + 32 * t * (D * 2), row_value + 32 * t, q0 + 32 * t);
     }
     // the second set's sums, 32 keys x D of FP32 a wave, dk and then dv
-    static_assert(4 * 32 * D * 4 <= 2 * SET, "the exchange fits");
+    static_assert(4 * 32 * D * 4 <= 4 * STAGE, "the exchange fits");
     f32x4* swap = reinterpret_cast<f32x4*>(lds_all) + wave * (32 * D / 4) + lane;
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
@@ -301,8 +337,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
                 }
     }
     if (set || w0 >= at.len) return;
-    store_row<D>(dk_row, dk, p.scale, lane, write);
-    store_row<D>(dv_row, dv, 1.0f, lane, write);
+    store();
 }
 
 } // namespace

@@ -54,7 +54,7 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16& s, int i0)
 // of 4 neighbouring chunks (the transposed one).
 // ------------------------------------------------------------------------
 template <int D>
-__device__ __forceinline__ uint32_t swizzle(uint32_t r)
+__device__ __forceinline__ constexpr uint32_t swizzle(uint32_t r)
 {
     return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
 }
@@ -92,6 +92,9 @@ __device__ __forceinline__ void publish()
 {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
+
+// All waves of the workgroup are here; copies stay in flight.
+__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
 // Every load into registers so far has landed, in a form that the compiler
 // sees: before a loop that issues copies, or its waits for those registers
@@ -139,6 +142,39 @@ __device__ __forceinline__ bf16x8 read_tr(const char* tile, int r0, int dt, int 
     union { s16x4 s[2]; bf16x8 v; } u;
     u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(tile + ra * (D * 2) + (c ^ fa) * 16 + 8 * (i & 1)));
     u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(tile + rb * (D * 2) + (c ^ fb) * 16 + 8 * (i & 1)));
+    return u.v;
+}
+
+// The same operands by LDS address.  A tile starts at a multiple of 256
+// bytes, so the swizzled chunk of step ks (of column block dt) is one XOR
+// away from that of step 0: a kernel short of registers keeps one address
+// for the tile instead of one for each step.
+typedef const __attribute__((address_space(3))) bf16x8* lds_operand;
+template <int D>
+__device__ __forceinline__ uint32_t rows_address(int lane)
+{
+    return (lane & 31) * (D * 2) + (((uint32_t)(lane >> 5) ^ swizzle<D>(lane & 31)) << 4);
+}
+__device__ __forceinline__ bf16x8 read_rows_at(uint32_t address, int ks, uint32_t offset)
+{
+    return *(lds_operand)(uintptr_t)((address ^ (ks << 5)) + offset);
+}
+template <int D>
+__device__ __forceinline__ uint32_t tr_address(int lane)
+{
+    const int half = lane >> 5, i = lane & 15;
+    const uint32_t r = 4 * half + (i >> 2), c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+    return r * (D * 2) + ((c ^ swizzle<D>(r)) << 4) + 8 * (i & 1);
+}
+template <int D>
+__device__ __forceinline__ bf16x8 read_tr_at(uint32_t address, int r0, int dt, uint32_t offset)
+{
+    // eight rows on, one bit of the swizzle differs
+    constexpr uint32_t flip = swizzle<D>(8) << 4;
+    union { s16x4 s[2]; bf16x8 v; } u;
+    const uint32_t a = address ^ (dt << 6);
+    u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(uintptr_t)(a + (r0 * (D * 2) + offset)));
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(uintptr_t)((a ^ flip) + ((r0 + 8) * (D * 2) + offset)));
     return u.v;
 }
 
