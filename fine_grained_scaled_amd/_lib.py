@@ -71,14 +71,6 @@ class FgsGemmOptions(ctypes.Structure):
     ]
 
 
-class FgsHeads(ctypes.Structure):
-    _fields_ = [
-        ("data", ctypes.c_void_p),
-        ("ld_token", ctypes.c_int64),
-        ("ld_head", ctypes.c_int64),
-    ]
-
-
 class FgsError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"fgs error {status}: {message}")
@@ -123,9 +115,10 @@ def load() -> ctypes.CDLL:
     lib.fgs_workspace_bytes.restype = SZ
     lib.fgs_gemm_workspace_bytes.argtypes = [I32, I64, I64]
     lib.fgs_gemm_workspace_bytes.restype = SZ
-    HP, F32 = ctypes.POINTER(FgsHeads), ctypes.c_float
-    lib.fgs_attention_fwd.argtypes = [HP, HP, HP, P, I32, I64, I32, I32, I32, F32, HP, P, P]
-    lib.fgs_attention_bwd.argtypes = [HP, HP, HP, HP, HP, P, P, I32, I64, I32, I32, I32, F32, HP, HP, HP, P, SZ, P]
+    F32 = ctypes.c_float
+    # fgs_heads (pointer, two 64-bit strides) goes as the address of three int64
+    lib.fgs_attention_fwd.argtypes = [P, P, P, P, I32, I64, I32, I32, I32, F32, P, P, P]
+    lib.fgs_attention_bwd.argtypes = [P, P, P, P, P, P, P, I32, I64, I32, I32, I32, F32, P, P, P, P, SZ, P]
     lib.fgs_attention_workspace_bytes.argtypes = [I64, I32]
     lib.fgs_attention_workspace_bytes.restype = SZ
     lib.fgs_residual_norm_fwd.argtypes = [P, I64, P, I64, I32, I64, I64, P, P, I64, I32, F32, P, F32, P, P, P]

@@ -10,18 +10,20 @@ attention(), whose backward pass captures like that of any torch function.
 """
 from __future__ import annotations
 
-import math
+import array
 from typing import Optional
 
 import torch
 
 from . import _lib
-from .ops import _ptr, _stream
+from .ops import _stream_of
 
 _LIMIT = "must be a [tokens x heads x head_dim] bfloat16 tensor"
+_HEADS = 24      # bytes of an fgs_heads: pointer and two strides
 
 
-def _heads(t: torch.Tensor, name: str) -> _lib.FgsHeads:
+def _heads(t: torch.Tensor, name: str):
+    """The fgs_heads of t: pointer, token stride, head stride."""
     if t.dtype != torch.bfloat16 or t.dim() != 3:
         raise TypeError(f"{name} {_LIMIT}")
     if not t.is_cuda:
@@ -29,21 +31,23 @@ def _heads(t: torch.Tensor, name: str) -> _lib.FgsHeads:
     token, head, value = t.stride()
     if value != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} must have unit stride along head_dim")
-    return _lib.FgsHeads(t.data_ptr(), token, head)
+    return t.data_ptr(), token, head
 
 
 def _check(q, k, v, cu_seqlens, softmax_scale):
     T, H, D = q.shape
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+    Tk, Hk, Dk = shape = k.shape
+    if shape != v.shape or Tk != T or Dk != D:
         raise ValueError(f"k and v must be [{T} x kv_heads x {D}] (got {tuple(k.shape)} and {tuple(v.shape)})")
-    if k.shape[1] == 0 or H % k.shape[1]:
-        raise ValueError(f"heads ({H}) must be a multiple of kv_heads ({k.shape[1]})")
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"heads ({H}) must be a multiple of kv_heads ({Hk})")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
             or cu_seqlens.numel() < 1:
         raise TypeError("cu_seqlens must be a contiguous 1-D int32 tensor of one entry at least")
-    if not (q.device == k.device == v.device == cu_seqlens.device):
+    gpu = q.get_device()
+    if k.get_device() != gpu or v.get_device() != gpu or cu_seqlens.get_device() != gpu:
         raise ValueError("q, k, v and cu_seqlens must be on one GPU")
-    return T, H, k.shape[1], D, (1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale))
+    return T, H, Hk, D, (D ** -0.5 if softmax_scale is None else float(softmax_scale))
 
 
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -53,12 +57,15 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     q is [T x H x D], k and v [T x Hk x D] (H a multiple of Hk, D 64 or 128),
     views of a fused projection among them.  softmax_scale: 1 / sqrt(D).
     Tokens of no sequence get out = 0 and lse = -inf."""
-    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    views = _heads(q, "q") + _heads(k, "k") + _heads(v, "v")
     T, H, Hk, D, scale = _check(q, k, v, cu_seqlens, softmax_scale)
     out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    _lib.check(_lib.load().fgs_attention_fwd(qs, ks, vs, _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, H, Hk, D, scale,
-                                             _heads(out, "out"), _ptr(lse), _stream()))
+    views = array.array("q", views + (out.data_ptr(), H * D, D))
+    at = views.buffer_info()[0]
+    _lib.check(_lib.load().fgs_attention_fwd(
+        at, at + _HEADS, at + 2 * _HEADS, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T, H, Hk, D, scale,
+        at + 3 * _HEADS, lse.data_ptr(), _stream_of(q)))
     return out, lse
 
 
@@ -69,25 +76,27 @@ def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     [T x H x D].  workspace: optional uint8 device scratch of
     fgs_attention_workspace_bytes() bytes.  The same inputs give the same
     bits; tokens of no sequence get zeros."""
-    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
-    os, gs = _heads(out, "out"), _heads(dout, "dout")
+    views = _heads(q, "q") + _heads(k, "k") + _heads(v, "v") + _heads(out, "out") + _heads(dout, "dout")
     T, H, Hk, D, scale = _check(q, k, v, cu_seqlens, softmax_scale)
     if out.shape != q.shape or dout.shape != q.shape:
         raise ValueError(f"out and dout must be {tuple(q.shape)} (got {tuple(out.shape)} and {tuple(dout.shape)})")
     if lse.dtype != torch.float32 or tuple(lse.shape) != (H, T) or not lse.is_contiguous():
         raise TypeError(f"lse must be a contiguous [{H} x {T}] float32 tensor")
-    if not (out.device == dout.device == lse.device == q.device):
+    gpu = q.get_device()
+    if out.get_device() != gpu or dout.get_device() != gpu or lse.get_device() != gpu:
         raise ValueError("all tensors must be on one GPU")
     dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k, v))
     lib = _lib.load()
     need = lib.fgs_attention_workspace_bytes(T, H)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
-    _lib.check(lib.fgs_attention_bwd(gs, qs, ks, vs, os, _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, H, Hk,
-                                     D, scale, _heads(dq, "dq"), _heads(dk, "dk"), _heads(dv, "dv"), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), _stream()))
+    elif workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same GPU")
+    views = array.array("q", views + (dq.data_ptr(), H * D, D, dk.data_ptr(), Hk * D, D, dv.data_ptr(), Hk * D, D))
+    at = [views.buffer_info()[0] + i * _HEADS for i in range(8)]
+    _lib.check(lib.fgs_attention_bwd(
+        at[4], *at[:4], lse.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T, H, Hk, D, scale, *at[5:],
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_of(q)))
     return dq, dk, dv
 
 

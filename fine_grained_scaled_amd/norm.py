@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from .ops import _need_gpu, _ptr, _stream
+from .ops import _need_gpu, _stream_of
 
 _RESIDUAL = {torch.float32: _lib.OUT_FP32, torch.bfloat16: _lib.OUT_BF16}
 
@@ -24,15 +24,19 @@ class ResidualNormGrads(NamedTuple):
     w_pre: torch.Tensor
 
 
+def _at(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
 def _matrix(t: torch.Tensor, name: str, shape, dtype) -> None:
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise TypeError(f"{name} must be a [{shape[0]} x {shape[1]}] {dtype} tensor (got {tuple(t.shape)} {t.dtype})")
     if t.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along columns")
 
 
 def _weight(t: Optional[torch.Tensor], name: str, width: int) -> None:
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (width,) or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.numel() != width or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous float32 tensor of {width} values")
 
 
@@ -40,14 +44,18 @@ def _check(y, x, w_post, gate, w_pre):
     """Shapes and types of the inputs; returns the gate's kind and row stride."""
     if y.dim() != 2:
         raise TypeError("y must be a [tokens x width] bfloat16 tensor")
-    shape = tuple(y.shape)
+    shape = y.shape
     if x.dtype not in _RESIDUAL:
         raise TypeError("the residual must be float32 or bfloat16")
     _matrix(y, "y", shape, torch.bfloat16)
     _matrix(x, "the residual", shape, x.dtype)
     _weight(w_pre, "w_pre", shape[1])
     _weight(w_post, "w_post", shape[1])
-    _need_gpu(y, x, w_post, gate, w_pre)
+    _need_gpu(y)
+    gpu = y.get_device()
+    for t in (x, w_pre, w_post, gate):
+        if t is not None and t.get_device() != gpu:
+            raise ValueError("all tensors must be on one GPU")
     if gate is None:
         return _lib.GATE_NONE, 0
     if gate.dim() == 1:
@@ -69,8 +77,8 @@ def residual_norm_fwd(y: torch.Tensor, x: torch.Tensor, *, w_pre: torch.Tensor, 
     r = torch.empty((T, W), dtype=x.dtype, device=y.device)
     n = torch.empty((T, W), dtype=torch.bfloat16, device=y.device)
     _lib.check(_lib.load().fgs_residual_norm_fwd(
-        _ptr(y), y.stride(0), _ptr(x), x.stride(0), _RESIDUAL[x.dtype], T, W, _ptr(w_post), _ptr(gate), ldg, kind,
-        alpha, _ptr(w_pre), eps, _ptr(r), _ptr(n), _stream()))
+        _at(y), y.stride(0), _at(x), x.stride(0), _RESIDUAL[x.dtype], T, W, _at(w_post), _at(gate), ldg, kind,
+        alpha, _at(w_pre), eps, _at(r), _at(n), _stream_of(y)))
     return r, n
 
 
@@ -84,9 +92,10 @@ def residual_norm_bwd(dr: torch.Tensor, dn: torch.Tensor, y: torch.Tensor, r: to
     fgs_residual_norm_workspace_bytes() bytes."""
     kind, ldg = _check(y, r, w_post, gate, w_pre)
     T, W = y.shape
-    _matrix(dr, "dr", (T, W), r.dtype)
-    _matrix(dn, "dn", (T, W), torch.bfloat16)
-    _need_gpu(dr, dn)
+    _matrix(dr, "dr", y.shape, r.dtype)
+    _matrix(dn, "dn", y.shape, torch.bfloat16)
+    if dr.get_device() != y.get_device() or dn.get_device() != y.get_device():
+        raise ValueError("all tensors must be on one GPU")
     dev = y.device
     dx = torch.empty((T, W), dtype=r.dtype, device=dev)
     dy = torch.empty((T, W), dtype=torch.bfloat16, device=dev)
@@ -96,12 +105,12 @@ def residual_norm_bwd(dr: torch.Tensor, dn: torch.Tensor, y: torch.Tensor, r: to
     lib = _lib.load()
     if workspace is None:
         workspace = torch.empty(lib.fgs_residual_norm_workspace_bytes(T, W), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same GPU")
     _lib.check(lib.fgs_residual_norm_bwd(
-        _ptr(dr), dr.stride(0), _ptr(dn), dn.stride(0), _ptr(y), y.stride(0), _ptr(r), r.stride(0), _RESIDUAL[r.dtype],
-        T, W, _ptr(w_post), _ptr(gate), ldg, kind, alpha, _ptr(w_pre), eps, _ptr(dx), _ptr(dy), _ptr(dgate),
-        _ptr(dw_post), _ptr(dw_pre), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()))
+        _at(dr), dr.stride(0), _at(dn), dn.stride(0), _at(y), y.stride(0), _at(r), r.stride(0), _RESIDUAL[r.dtype],
+        T, W, _at(w_post), _at(gate), ldg, kind, alpha, _at(w_pre), eps, _at(dx), _at(dy), _at(dgate),
+        _at(dw_post), _at(dw_pre), _at(workspace), workspace.numel() * workspace.element_size(), _stream_of(y)))
     return ResidualNormGrads(dx, dy, dgate, dw_post, dw_pre)
 
 

@@ -29,6 +29,17 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of t's GPU as a raw handle, which must be the
+    current GPU (kernels are launched there).  The raw lookup takes 0.3 us
+    where a torch.cuda.Stream object takes 2.5, which counts beside calls of
+    a few microseconds."""
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on GPU {device}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _need_gpu(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
