@@ -10,11 +10,22 @@
 // share the key head.  p and ds are recomputed in FP32 and rounded to BF16
 // once for the products; all sums are FP32.
 //
+// A row's p is about 1 / (its keys), so the first rows of a sequence weigh
+// most in every gradient, and there dout . v - delta cancels: row 0 has
+// ds = 0.  The rows that see one tile of keys (the first 64) therefore take
+// delta from their own p and dout . v instead of the rounded out, and hand
+// p and ds to the products as two BF16 terms, value and remainder.  That is
+// one more set of products in one tile of a sequence, and it takes the error
+// of dq, dk and dv against 64 bits from 1.5 to 1.3 times that of the results'
+// own rounding.
+//
 // Two kernels, each with its sums in registers: one owns query rows (dq, and
 // delta), the other owns keys (dk, dv) and walks the query heads of their
 // group.  They compute the scores twice, 14 D operations a pair instead of
 // 10, and in return no sum crosses workgroups: no atomics, no FP32 copy of
 // dq, and the same bits on every run.
+#include <type_traits>
+
 #include "attention_device.h"
 
 namespace fgs {
@@ -41,11 +52,22 @@ struct BwdParams {
 constexpr int BN = 64;    // keys a tile of the dq kernel
 constexpr int QN = 64;    // query rows a tile of the dk, dv kernel
 constexpr int KN = 128;   // keys a workgroup of it
+constexpr int FIRST = 64; // rows at the start of a sequence that are kept more exactly
+static_assert(FIRST == BN && FIRST <= KN && FIRST == QN && KN <= 2 * BN, "one tile of keys, one of queries");
+
+// What pack8() drops, rounded in turn.
+__device__ __forceinline__ bf16x8 pack8_rest(const f32x16& s, int i0)
+{
+    bf16x8 r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = (__bf16)(s[i0 + j] - (float)(__bf16)s[i0 + j]);
+    return r;
+}
 
 // dq: 4 waves as in the forward kernel (HB heads x 128 / HB tokens, 32 rows a
 // wave), S^T = K Q^T and dP^T = V dO^T a 32-key step, dQ^T += K^T dS^T.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdParams p)
 {
     constexpr int TILE = BN * D * 2;
     __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
@@ -95,15 +117,11 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
     const float lse = p.lse[head * p.T + token];
     const float from = lse == -__builtin_inff() ? 0.0f : -lse / p.scale;
     delta = -delta;
-    if (write && half == 0) {
-        p.ws[head * p.T + token] = from;
-        p.ws[(p.H + head) * p.T + token] = delta;
-    }
 
     const uint32_t base = lds_offset(lds);
     const int last = at.len - 1;
     const int n_tiles = (min(t0 + rows, at.len) + BN - 1) / BN;
-    const int wave_keys = w0 < at.len ? min(w0 + 32, at.len) : 0;
+    const int wave_keys = w0 >= FIRST && w0 < at.len ? min(w0 + 32, at.len) : 0;   // the first rows come after the loop
     const float c = p.scale * LOG2E;
     auto load = [&](int n, int buf) {
         const int k0 = n * BN;
@@ -149,12 +167,51 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(BwdParams p)
         }
     }
     if (w0 >= at.len) return;
+    if (w0 < FIRST) {                                  // their tile is still in LDS
+        f32x16 s[2], dp[2];
+        float sum = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] = from, dp[t][i] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                s[t] = mfma(read_rows<D>(lds, 32 * t, ks, lane), q[ks], s[t]);
+                dp[t] = mfma(read_rows<D>(lds + 2 * TILE, 32 * t, ks, lane), g[ks], dp[t]);
+            }
+            const int seen = min(row, last) - 32 * t - 4 * half;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[t][i] = acc_row(i, 0) > seen ? 0.0f : __builtin_amdgcn_exp2f(s[t][i] * c);
+                dp[t][i] = acc_row(i, 0) > seen ? 0.0f : dp[t][i];
+                sum = __builtin_fmaf(s[t][i], dp[t][i], sum);
+            }
+        }
+        delta = -(sum + swap_half(sum));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] *= dp[t][i] + delta;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 ds = pack8(s[t], 8 * ks), rest = pack8_rest(s[t], 8 * ks);
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt) {
+                    const bf16x8 x = read_tr<D>(lds, 32 * t + 16 * ks, dt, lane);
+                    dq[dt] = mfma(x, ds, mfma(x, rest, dq[dt]));
+                }
+            }
+        }
+    }
+    if (write && half == 0) {
+        p.ws[head * p.T + token] = from;
+        p.ws[(p.H + head) * p.T + token] = delta;
+    }
     store_row<D>(dq_row, dq, p.scale, lane, write);
 }
 
 // dk and dv: 8 waves, two sets of 4 that own the same 4 x 32 keys, whose key
-// rows stay in registers, and whose value rows do as far as 256 registers
-// reach (the other half lies in LDS).  Tiles of 64 query rows and their
+// and value rows stay in registers.  Tiles of 64 query rows and their
 // gradients pass through LDS, head after head of the group, the sets taking
 // turns; at the end the second set hands its sums to the first through LDS.
 // So a workgroup fills a compute unit with two waves a SIMD and the longest
@@ -228,11 +285,12 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
             g2lds4(uniform_ptr(p.ws + ((int64_t)wave * p.H + head) * p.T + at.start + q0),
                    4 * min(lane & (QN - 1), last - q0), to + 2 * TILE + wave * 256);
     };
-    // 32 queries and the wave's 32 keys.  256 registers hold the sums, the
+    // 32 queries and the wave's 32 keys, with p and ds or with what their
+    // rounding leaves.  256 registers hold the sums, the
     // keys and values and two score tiles with little to spare: operands are
     // read two products ahead, which the scheduler barriers keep in place.
     const uint32_t rows_at = rows_address<D>(lane), tr_at = tr_address<D>(lane);
-    auto step = [&](uint32_t tile, const float* row_value, int q0) {
+    auto step = [&](auto rest, uint32_t tile, const float* row_value, int q0) {
         f32x16 s, dp;
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
@@ -282,6 +340,10 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
             for (int i = 0; i < 16; ++i)
                 if (acc_row(i, 0) < from || acc_row(i, 0) >= to) s[i] = dp[i] = 0.0f;
         }
+        if constexpr (decltype(rest)::value) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] -= (float)(__bf16)s[i], dp[i] -= (float)(__bf16)dp[i];
+        }
         bf16x8 pr[2], ds[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) pr[ks] = pack8(s, 8 * ks), ds[ks] = pack8(dp, 8 * ks);
@@ -309,7 +371,20 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
 #pragma unroll
         for (int t = 0; t < QN / 32; ++t)
             if (q0 + 32 * t + 31 >= w0 && q0 + 32 * t < at.len)
-                step(tile + 32 * t * (D * 2), row_value + 32 * t, q0 + 32 * t);
+                step(std::false_type{}, tile + 32 * t * (D * 2), row_value + 32 * t, q0 + 32 * t);
+    }
+    // the first rows' remainders, head after head; not in the loop above,
+    // where the choice alone cost 10%
+    for (int h = set; k0 < FIRST && h < p.group_heads + set; h += 2) {
+        publish();
+        if (h < p.group_heads) load(kv_head * p.group_heads + h, 0, 0);
+        publish();
+        if (h >= p.group_heads) continue;
+        const float* row_value = reinterpret_cast<const float*>(lds + 2 * TILE) + 4 * half;
+#pragma unroll 1
+        for (int q0 = 0; q0 < FIRST; q0 += 32)
+            if (q0 + 31 >= w0 && q0 < at.len)
+                step(std::true_type{}, base + q0 * (D * 2), row_value + q0, q0);
     }
     // the second set's sums, 32 keys x D of FP32 a wave, dk and then dv
     static_assert(4 * 32 * D * 4 <= 4 * STAGE, "the exchange fits");

@@ -226,7 +226,18 @@ __device__ __forceinline__ int64_t segment_start(const int32_t* cu, int S, int64
 __device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, int rows, int tile, int lane)
 {
     // every lane tests one segment: how many start at or before this tile
+    Where w;
     int n = 0;
+    if (S + 2 < 64) {                   // and keeps its start: one read of cu in all
+        const int start = (int)segment_start(cu, S, T, lane);
+        const int seg = __popcll(__ballot(lane < S + 2 && start / rows + lane <= tile)) - 1;
+        const int a = __builtin_amdgcn_readlane(start, seg), b = __builtin_amdgcn_readlane(start, seg + 1);
+        w.start = a;
+        w.tile = tile - (a / rows + seg);
+        w.len = b > a && w.tile >= 0 ? b - a : 0;
+        w.sequence = seg > 0 && seg <= S;
+        return w;
+    }
     for (int i0 = 0; i0 < S + 2; i0 += 64) {
         const int i = i0 + lane;
         const bool before = i < S + 2 && (int)(segment_start(cu, S, T, i) / rows) + i <= tile;
@@ -234,7 +245,6 @@ __device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, 
     }
     const int seg = __builtin_amdgcn_readfirstlane(n - 1);
     const int64_t a = segment_start(cu, S, T, seg), b = segment_start(cu, S, T, seg + 1);
-    Where w;
     w.start = __builtin_amdgcn_readfirstlane((int)a);
     w.tile = __builtin_amdgcn_readfirstlane(tile - ((int)(a / rows) + seg));
     w.len = __builtin_amdgcn_readfirstlane(b > a && w.tile >= 0 ? (int)(b - a) : 0);
@@ -242,66 +252,80 @@ __device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, 
     return w;
 }
 
+// The sum over the wave of non-negative values, in every lane.
+__device__ __forceinline__ int wave_total(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, DPP_XOR1, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, DPP_XOR2, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, DPP_HALF_MIRROR, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, DPP_MIRROR, 0xF, 0xF, false);
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = (int)(a[0] + a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __builtin_amdgcn_readfirstlane((int)(b[0] + b[1]));
+}
+
 // The same tiles by the work they stand for, most first: a tile that is the
 // m-th of its segment counted from the cheap end (the first query tile sees
 // the fewest keys, the last key tile is seen by the fewest queries) has size
 // m, and workgroup `rank` takes the rank-th tile in order of falling size, so
 // that the longest workgroups start first and the shortest fill the end.
-// Up to SORTED - 2 sequences; each lane holds a few segments.
+// Up to SORTED - 2 sequences; each lane holds a few segments, whose bounds
+// are read once.
 constexpr int SORTED = 256;
 template <bool KEYS>
 __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int64_t T, int rows, int rank, int lane)
 {
     constexpr int C = SORTED / 64;
-    int n[C], most = 0;
+    int start[C], len[C], n[C], segments = 0;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const int i = 64 * j + lane;
-        n[j] = 0;
+        start[j] = len[j] = n[j] = 0;
         if (64 * j < S + 2 && i < S + 2) {
-            const int64_t len = segment_start(cu, S, T, i + 1) - segment_start(cu, S, T, i);
-            n[j] = len > 0 ? (int)((len + rows - 1) / rows) : 0;
-            most = max(most, n[j]);
+            const int64_t a = segment_start(cu, S, T, i), b = segment_start(cu, S, T, i + 1);
+            start[j] = (int)a;
+            len[j] = b > a ? (int)(b - a) : 0;
+            n[j] = (int)(((uint32_t)len[j] + rows - 1) / (uint32_t)rows);
         }
+        segments += __popcll(__ballot(n[j] > 0));
     }
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) most = max(most, __shfl_xor(most, m));
-    most = __builtin_amdgcn_readfirstlane(most);
     auto larger = [&](int m) {          // tiles of a size above m
         int v = 0;
 #pragma unroll
         for (int j = 0; j < C; ++j) v += max(n[j] - m, 0);
-#pragma unroll
-        for (int k = 1; k < 64; k *= 2) v += __shfl_xor(v, k);
-        return __builtin_amdgcn_readfirstlane(v);
+        return wave_total(v);
     };
     Where w{0, 0, 0, false};
-    if (rank >= larger(0)) return w;
-    int lo = 1, hi = most;              // the smallest m with at most `rank` larger tiles
-    while (lo < hi) {
-        const int m = (lo + hi) / 2;
-        if (larger(m) <= rank) hi = m;
-        else lo = m + 1;
+    const int all = larger(0);
+    if (rank >= all) return w;
+    int size, r = 0;
+    if (segments == 1) {
+        size = all - rank;              // one sequence: its tiles in order
+    } else {
+        int lo = 1, hi = all;           // the smallest size with at most `rank` larger tiles
+        while (lo < hi) {
+            const int m = (lo + hi) / 2;
+            if (larger(m) <= rank) hi = m;
+            else lo = m + 1;
+        }
+        size = lo;
+        r = rank - larger(size);
     }
-    int r = rank - larger(lo), seg = 0, tiles = 0;
 #pragma unroll
     for (int j = 0; j < C; ++j) {       // the r-th segment that has a tile of this size
-        const uint64_t has = __ballot(n[j] >= lo);
+        const uint64_t has = __ballot(n[j] >= size);
         const int c = __popcll(has), before = __popcll(has & ((1ull << lane) - 1));
-        const uint64_t hit = __ballot(n[j] >= lo && before == r);
+        const uint64_t hit = __ballot(n[j] >= size && before == r);
         if (r >= 0 && r < c) {
-            const int at = __ffsll((unsigned long long)hit) - 1;
-            seg = 64 * j + at;
-            tiles = __builtin_amdgcn_readlane(n[j], at);
+            const int at = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+            w.start = __builtin_amdgcn_readlane(start[j], at);
+            w.len = __builtin_amdgcn_readlane(len[j], at);
+            w.tile = KEYS ? __builtin_amdgcn_readlane(n[j], at) - size : size - 1;
+            w.sequence = 64 * j + at > 0 && 64 * j + at <= S;
         }
         r -= c;
     }
-    seg = __builtin_amdgcn_readfirstlane(seg);
-    const int64_t a = segment_start(cu, S, T, seg), b = segment_start(cu, S, T, seg + 1);
-    w.start = __builtin_amdgcn_readfirstlane((int)a);
-    w.len = __builtin_amdgcn_readfirstlane((int)(b - a));
-    w.tile = __builtin_amdgcn_readfirstlane(KEYS ? tiles - lo : lo - 1);
-    w.sequence = seg > 0 && seg <= S;
     return w;
 }
 
@@ -322,6 +346,8 @@ __device__ __forceinline__ Mine my_tile(const int32_t* cu, int S, int64_t T, int
         m.group = b % groups;
         rank = b / groups;
     }
+    // queries go by their place: by size, neighbours come from different
+    // sequences and share no keys (61 prompts: 46.0 -> 49.2 us)
     if (KEYS && S + 2 <= SORTED) m.at = find_tile_by_size<KEYS>(cu, S, T, rows, rank, lane);
     else m.at = find_tile(cu, S, T, rows, KEYS ? rank : tiles - 1 - rank, lane);
     return m;
