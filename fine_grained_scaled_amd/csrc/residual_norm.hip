@@ -20,6 +20,11 @@
 // the weights are read once; the next row's loads are issued before this
 // row's sums.  Sums over rows stay in registers, one partial row a workgroup,
 // and a second kernel adds the partial rows in a fixed order.
+// Measured (a 2 GiB copy reaches 4.87 TB/s): forward 8192 x 16384, FP32
+// residual, 302 us, 5.3 TB/s; backward 8192 x 4096, BF16 residual, 88 us,
+// 4.6 TB/s with the sums' 5 us; backward 4111 x 7168, FP32 residual and a gate
+// for each token, 135 us, 4.8 TB/s; backward rows of more than 8192 values
+// reach 2.9 to 4.6 TB/s, bound by their weights' reads from L2.
 #include <algorithm>
 
 #include "fgs_device.h"
@@ -121,6 +126,7 @@ struct NormParams {
     float* partial;         // [workgroups][3][W]: dw_pre, dw_post, dgate
     int64_t T, ldy, ldx, ldg, lddr, lddn;
     int W;
+    int row_threads;        // backward: threads a row; a workgroup takes blockDim / row_threads rows at once
     float alpha, eps, inv_w;
 };
 
@@ -208,157 +214,341 @@ __global__ __launch_bounds__(1024) void residual_norm_fwd_kernel(NormParams p)
     }
 }
 
-template <int VPT, bool FP32, bool POST, int GATE>
-__global__ __launch_bounds__(512) void residual_norm_bwd_kernel(NormParams p)
+// Half h of 8 values as loaded.
+template <bool FP32>
+__device__ __forceinline__ void unpack4(const Raw<FP32>& r, int h, float f[4])
 {
-    __shared__ float slots[2][3 * 16];
-    const int vecs = p.W / 8, step = blockDim.x;
-    float a_pre[VPT][8], a_post[VPT][8], a_gate[VPT][8];
-    Raw<false> y[VPT], dn[VPT], gt[VPT];
-    Raw<FP32> r[VPT], dr[VPT];
-    // without a post norm, y is needed for the gate's gradient alone
-    constexpr bool NEED_Y = POST || GATE != GATE_NONE;
-    auto load = [&](int64_t row) {
+    if constexpr (FP32) {
+        f[0] = as_f32(r.v[h].x), f[1] = as_f32(r.v[h].y), f[2] = as_f32(r.v[h].z), f[3] = as_f32(r.v[h].w);
+    } else {
+        const uint32_t a = h ? r.v[0].z : r.v[0].x, b = h ? r.v[0].w : r.v[0].y;
+        f[0] = bf16_lo(a), f[1] = bf16_hi(a), f[2] = bf16_lo(b), f[3] = bf16_hi(b);
+    }
+}
+template <bool FP32>
+__device__ __forceinline__ void pack4(Raw<FP32>& r, int h, const float f[4])
+{
+    if constexpr (FP32) {
+        r.v[h] = make_uint4(as_u32(f[0]), as_u32(f[1]), as_u32(f[2]), as_u32(f[3]));
+    } else {
+        (h ? r.v[0].z : r.v[0].x) = pack2(f[0], f[1]);
+        (h ? r.v[0].w : r.v[0].y) = pack2(f[2], f[3]);
+    }
+}
+// A row's address, the same in every lane, and 8 values of it by their 32-bit
+// place: one scalar address a tensor instead of a vector one for each access.
+template <bool FP32>
+__device__ __forceinline__ char* row_of(const void* base, int64_t row, int64_t ld)
+{
+    return const_cast<char*>(static_cast<const char*>(base)) + row * ld * (FP32 ? 4 : 2);
+}
+template <bool FP32>
+__device__ __forceinline__ Raw<FP32> load_at(const char* row, int c)
+{
+    Raw<FP32> r;
+    const uint4* p = reinterpret_cast<const uint4*>(row + (uint32_t)(c * (FP32 ? 32 : 16)));
+    r.v[0] = p[0];
+    if constexpr (FP32) r.v[1] = p[1];
+    return r;
+}
+template <bool FP32>
+__device__ __forceinline__ void store_at(char* row, int c, const Raw<FP32>& r)
+{
+    uint4* p = reinterpret_cast<uint4*>(row + (uint32_t)(c * (FP32 ? 32 : 16)));
+    p[0] = r.v[0];
+    if constexpr (FP32) p[1] = r.v[1];
+}
+__device__ __forceinline__ void load4(const float* p, float f[4])
+{
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+
+// One barrier a row: with a = gate w_post y and b = dn w_pre, the sum that dy
+// needs is linear in d,
+//   sum a d = sum a dr + (sum a b - c1 / rms(r) sum a r) / rms(r),
+// so all six row sums (r^2, b r, y^2 and these three) come from one pass over
+// the row's registers, and the second pass writes every output.  The weights
+// lie in LDS (read again for each row from L2 they cost more than the row
+// itself: 8192 x 4096 with every option 102 us, and 4.1 against 5.1 TB/s for
+// an FP32 residual), and the next row's loads are issued before this row's
+// sums.  A workgroup fills a compute unit, so that 256 partial rows are all
+// that the second kernel has to add; narrow rows go several at a time.
+template <int VPT, bool FP32, bool POST, int GATE>
+__global__ __launch_bounds__(1024) void residual_norm_bwd_kernel(NormParams p)
+{
+    // a wide row, two vectors a thread, needs the registers of two sums: LDS
+    // holds these instead of the weights
+    constexpr bool WIDE = VPT > 1;
+    constexpr bool CHANNEL = GATE == GATE_CHANNEL;
+    constexpr bool NEED_Y = POST || GATE != GATE_NONE;   // without a post norm, for the gate's gradient alone
+    constexpr int SUMS = POST ? 6 : 2;
+    extern __shared__ float4 lds4[];
+    __shared__ float slots[2][6][16];
+    float* lds = reinterpret_cast<float*>(lds4);
+    const float* w_pre = WIDE ? p.w_pre : lds;
+    const float* w_post = WIDE ? p.w_post : lds + p.W;
+    const float* w_gate = WIDE ? static_cast<const float*>(p.gate) : lds + (POST ? 2 : 1) * p.W;
+    float *wide_post = lds, *wide_gate = lds + (POST ? p.W : 0);
+
+    const int vecs = p.W / 8, step = p.row_threads;
+    const int waves = step >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int slot = wave / waves, at_once = (int)(blockDim.x >> 6) / waves;
+    const int c0 = threadIdx.x - slot * step;
+    for (int i = threadIdx.x; i < p.W / 4; i += blockDim.x) {
+        if (WIDE) {
+            if (POST) lds4[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (CHANNEL) lds4[(POST ? p.W / 4 : 0) + i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            continue;
+        }
+        lds4[i] = reinterpret_cast<const float4*>(p.w_pre)[i];
+        if (POST) lds4[p.W / 4 + i] = reinterpret_cast<const float4*>(p.w_post)[i];
+        if (CHANNEL) lds4[(POST ? 2 : 1) * (p.W / 4) + i] = reinterpret_cast<const float4*>(p.gate)[i];
+    }
+
+    struct Row { Raw<false> y[VPT], dn[VPT], g[VPT]; Raw<FP32> r[VPT], dr[VPT]; };
+    auto load = [&](Row& to, int64_t row) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * step;
-            if (c >= vecs) break;
-            if (NEED_Y) y[j] = load8<false>(p.y, row * p.ldy + 8 * c);
-            r[j] = load8<FP32>(p.x, row * p.ldx + 8 * c);
-            dn[j] = load8<false>(p.dn, row * p.lddn + 8 * c);
-            dr[j] = load8<FP32>(p.dr, row * p.lddr + 8 * c);
-            if (GATE == GATE_TOKEN) gt[j] = load8<false>(p.gate, row * p.ldg + 8 * c);
+            const int c = c0 + j * step;
+            if (c >= vecs || row >= p.T) break;
+            to.r[j] = load_at<FP32>(row_of<FP32>(p.x, row, p.ldx), c);
+            to.dn[j] = load_at<false>(row_of<false>(p.dn, row, p.lddn), c);
+            if (NEED_Y) to.y[j] = load_at<false>(row_of<false>(p.y, row, p.ldy), c);
+            to.dr[j] = load_at<FP32>(row_of<FP32>(p.dr, row, p.lddr), c);
+            if (GATE == GATE_TOKEN) to.g[j] = load_at<false>(row_of<false>(p.gate, row, p.ldg), c);
         }
     };
-    int64_t row = blockIdx.x;
-    load(row);
+    auto gate_of = [&](const Row& now, int j, int c, int h, float g[4]) {
+        if (GATE == GATE_TOKEN) unpack4<false>(now.g[j], h, g);
+        else if (CHANNEL) load4(w_gate + (uint32_t)(8 * c + 4 * h), g);
+    };
+    float a_pre[VPT][8], a_post[VPT][8], a_gate[VPT][8];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) a_pre[j][i] = a_post[j][i] = a_gate[j][i] = 0.0f;
-    for (; row < p.T; row += gridDim.x) {
-        float sum[3] = {0.0f, 0.0f, 0.0f};      // r^2, dn w_pre r, y^2
+    auto to_lds = [](float* at, const float f[4]) { *reinterpret_cast<float4*>(at) = make_float4(f[0], f[1], f[2], f[3]); };
+
+    auto one = [&](Row& now, int64_t row, int parity) {
+        float sum[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * step;
-            if (c >= vecs) break;
-            float w[8], f[8], d[8], v[8];
-            unpack<true>(load8<true>(p.w_pre, 8 * c), w);
-            unpack<FP32>(r[j], f);
-            unpack<false>(dn[j], d);
-            if (POST) unpack<false>(y[j], v);
+            const int c = c0 + j * step;
+            if (c >= vecs || row >= p.T) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sum[0] = __builtin_fmaf(f[i], f[i], sum[0]);
-                sum[1] = __builtin_fmaf(d[i] * w[i], f[i], sum[1]);
-                if (POST) sum[2] = __builtin_fmaf(v[i], v[i], sum[2]);
+            for (int h = 0; h < 2; ++h) {
+                float w[4], r[4], b[4], y[4], wp[4], g[4], dr[4];
+                load4(w_pre + (uint32_t)(8 * c + 4 * h), w);
+                unpack4<FP32>(now.r[j], h, r);
+                unpack4<false>(now.dn[j], h, b);
+                if (POST) {
+                    unpack4<false>(now.y[j], h, y);
+                    load4(w_post + (uint32_t)(8 * c + 4 * h), wp);
+                    unpack4<FP32>(now.dr[j], h, dr);
+                    gate_of(now, j, c, h, g);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    b[i] *= w[i];
+                    sum[0] = __builtin_fmaf(r[i], r[i], sum[0]);
+                    sum[1] = __builtin_fmaf(b[i], r[i], sum[1]);
+                    if (POST) {
+                        const float a = GATE == GATE_NONE ? wp[i] * y[i] : g[i] * wp[i] * y[i];
+                        sum[2] = __builtin_fmaf(y[i], y[i], sum[2]);
+                        sum[3] = __builtin_fmaf(a, dr[i], sum[3]);
+                        sum[4] = __builtin_fmaf(a, b[i], sum[4]);
+                        sum[5] = __builtin_fmaf(a, r[i], sum[5]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        block_sum(sum, slots[0]);
+#pragma unroll
+        for (int k = 0; k < SUMS; ++k) sum[k] = wave_sum(sum[k]);
+        if (waves > 1) {
+            // slots alternate from row to row, so one barrier is enough
+            if (lane == 0)
+#pragma unroll
+                for (int k = 0; k < SUMS; ++k) slots[parity][k][wave] = sum[k];
+            __syncthreads();
+            const int w = lane & 15;
+#pragma unroll
+            for (int k = 0; k < SUMS; ++k) {
+                float v = w < waves ? slots[parity][k][slot * waves + w] : 0.0f;
+                v = dpp_add<DPP_XOR1>(v);
+                v = dpp_add<DPP_XOR2>(v);
+                v = dpp_add<DPP_HALF_MIRROR>(v);
+                sum[k] = dpp_add<DPP_MIRROR>(v);
+            }
+        }
+        if (row >= p.T) return;
         const float rr = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], p.inv_w, p.eps));
         const float c1 = sum[1] * rr * p.inv_w;
         const float ry = POST ? __builtin_amdgcn_rsqf(__builtin_fmaf(sum[2], p.inv_w, p.eps)) : 1.0f;
-        float t[VPT][8], sum2[1] = {0.0f};
+        const float c2 = POST ? (sum[3] + rr * (sum[4] - c1 * rr * sum[5])) * ry * p.inv_w : 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * step;
+            const int c = c0 + j * step;
             if (c >= vecs) break;
-            float w[8], f[8], d[8], v[8], g[8], wp[8], dx[8];
-            unpack<true>(load8<true>(p.w_pre, 8 * c), w);
-            unpack<FP32>(r[j], f);
-            unpack<false>(dn[j], d);
-            unpack<FP32>(dr[j], dx);
-            if (NEED_Y) unpack<false>(y[j], v);
-            if (POST) unpack<true>(load8<true>(p.w_post, 8 * c), wp);
-            if (GATE == GATE_CHANNEL) unpack<true>(load8<true>(p.gate, 8 * c), g);
-            if (GATE == GATE_TOKEN) unpack<false>(gt[j], g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float fh = f[i] * rr;
-                a_pre[j][i] = __builtin_fmaf(d[i], fh, a_pre[j][i]);
-                const float dd = __builtin_fmaf(rr, __builtin_fmaf(-fh, c1, d[i] * w[i]), dx[i]);
-                dx[i] = p.alpha * dd;
-                const float yh = POST ? v[i] * ry : 0.0f;
-                if (GATE != GATE_NONE) {
-                    const float dg = dd * (POST ? yh * wp[i] : v[i]);
-                    if (GATE == GATE_CHANNEL) a_gate[j][i] += dg;
-                    else f[i] = dg;
-                }
-                float dz = GATE == GATE_NONE ? dd : dd * g[i];
-                if (POST) {
-                    a_post[j][i] = __builtin_fmaf(dz, yh, a_post[j][i]);
-                    dz *= wp[i];
-                    sum2[0] = __builtin_fmaf(dz, v[i], sum2[0]);
-                }
-                t[j][i] = dz;
+            // two vectors of every input, sums and outputs pass 128 registers:
+            // the gate is read again, and with every option on FP32 rows are
+            // (4096 x 16384: 449 -> 417 us; without a gate 315 -> 345, so there not)
+            if (WIDE && FP32 && POST && GATE != GATE_NONE) {
+                now.r[j] = load_at<FP32>(row_of<FP32>(p.x, row, p.ldx), c);
+                now.dr[j] = load_at<FP32>(row_of<FP32>(p.dr, row, p.lddr), c);
             }
-            store8<FP32>(p.dx, row * p.W + 8 * c, dx);
-            if (GATE == GATE_TOKEN) store8<false>(p.dgate, row * p.W + 8 * c, f);
-        }
-        float c2 = 0.0f;
-        if (POST) {
-            block_sum(sum2, slots[1]);
-            c2 = sum2[0] * ry * p.inv_w;
-        }
+            if (WIDE && GATE == GATE_TOKEN) now.g[j] = load_at<false>(row_of<false>(p.gate, row, p.ldg), c);
+            Raw<FP32> dx_out;
+            Raw<false> dy_out, dg_out;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * step;
-            if (c >= vecs) break;
-            if (POST) {
-                float v[8];
-                unpack<false>(y[j], v);
+            for (int h = 0; h < 2; ++h) {
+                float w[4], r[4], dn[4], y[4], wp[4], g[4], d[4], dg[4], dy[4];
+                load4(w_pre + (uint32_t)(8 * c + 4 * h), w);
+                if (POST) load4(w_post + (uint32_t)(8 * c + 4 * h), wp);
+                unpack4<FP32>(now.r[j], h, r);
+                unpack4<false>(now.dn[j], h, dn);
+                unpack4<FP32>(now.dr[j], h, d);
+                if (NEED_Y) unpack4<false>(now.y[j], h, y);
+                gate_of(now, j, c, h, g);
+                float *sum_post = a_post[j] + 4 * h, *sum_gate = a_gate[j] + 4 * h;
+                float wide_p[4], wide_g[4];
+                if (WIDE && POST) load4(wide_post + (uint32_t)(8 * c + 4 * h), sum_post = wide_p);
+                if (WIDE && CHANNEL) load4(wide_gate + (uint32_t)(8 * c + 4 * h), sum_gate = wide_g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t[j][i] = ry * __builtin_fmaf(-v[i] * ry, c2, t[j][i]);
+                for (int i = 0; i < 4; ++i) {
+                    const float rh = r[i] * rr;
+                    a_pre[j][4 * h + i] = __builtin_fmaf(dn[i], rh, a_pre[j][4 * h + i]);
+                    const float dd = __builtin_fmaf(rr, __builtin_fmaf(-rh, c1, dn[i] * w[i]), d[i]);
+                    d[i] = p.alpha * dd;
+                    const float yh = POST ? y[i] * ry : 0.0f;
+                    if (GATE != GATE_NONE) {
+                        const float z = POST ? yh * wp[i] : y[i];
+                        if (CHANNEL) sum_gate[i] = __builtin_fmaf(dd, z, sum_gate[i]);
+                        else dg[i] = dd * z;
+                    }
+                    float dz = GATE == GATE_NONE ? dd : dd * g[i];
+                    if (POST) {
+                        sum_post[i] = __builtin_fmaf(dz, yh, sum_post[i]);
+                        dz = ry * __builtin_fmaf(-yh, c2, dz * wp[i]);
+                    }
+                    dy[i] = dz;
+                }
+                if (WIDE && POST) to_lds(wide_post + (uint32_t)(8 * c + 4 * h), wide_p);
+                if (WIDE && CHANNEL) to_lds(wide_gate + (uint32_t)(8 * c + 4 * h), wide_g);
+                pack4<FP32>(dx_out, h, d);
+                pack4<false>(dy_out, h, dy);
+                if (GATE == GATE_TOKEN) pack4<false>(dg_out, h, dg);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            store8<false>(p.dy, row * p.W + 8 * c, t[j]);
+            store_at<FP32>(row_of<FP32>(p.dx, row, p.W), c, dx_out);
+            store_at<false>(row_of<false>(p.dy, row, p.W), c, dy_out);
+            if (GATE == GATE_TOKEN) store_at<false>(row_of<false>(p.dgate, row, p.W), c, dg_out);
         }
-        if (row + gridDim.x < p.T) load(row + gridDim.x);
-        if (!POST && blockDim.x > 64) __syncthreads();
+    };
+
+    // every wave of the workgroup takes as many turns, with or without a row
+    const int64_t stride = (int64_t)gridDim.x * at_once;
+    int64_t first = (int64_t)blockIdx.x * at_once;
+    int parity = 0;
+    Row now, next;
+    load(now, first + slot);
+    __syncthreads();
+    for (; first < p.T; first += stride) {
+        if constexpr (VPT == 1) {
+            load(next, first + stride + slot);
+            one(now, first + slot, parity);
+            now = next;
+        } else {
+            one(now, first + slot, parity);
+            load(now, first + stride + slot);
+        }
+        parity ^= 1;
     }
+    // the rows' sums, slot after slot through LDS
+    for (int s = 1; s < at_once; ++s) {
+        __syncthreads();
+        if (slot == s && c0 < vecs) {
+            store8<true>(lds, 8 * c0, a_pre[0]);
+            if (POST) store8<true>(lds, p.W + 8 * c0, a_post[0]);
+            if (CHANNEL) store8<true>(lds, (POST ? 2 : 1) * p.W + 8 * c0, a_gate[0]);
+        }
+        __syncthreads();
+        if (slot == 0 && c0 < vecs) {
+            float f[8];
+            unpack<true>(load8<true>(lds, 8 * c0), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a_pre[0][i] += f[i];
+            if (POST) {
+                unpack<true>(load8<true>(lds, p.W + 8 * c0), f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a_post[0][i] += f[i];
+            }
+            if (CHANNEL) {
+                unpack<true>(load8<true>(lds, (POST ? 2 : 1) * p.W + 8 * c0), f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a_gate[0][i] += f[i];
+            }
+        }
+    }
+    if (slot != 0) return;
     float* out = p.partial + (int64_t)blockIdx.x * 3 * p.W;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = threadIdx.x + j * step;
+        const int c = c0 + j * step;
         if (c >= vecs) break;
+        if (WIDE && POST) unpack<true>(load8<true>(wide_post, 8 * c), a_post[j]);
+        if (WIDE && CHANNEL) unpack<true>(load8<true>(wide_gate, 8 * c), a_gate[j]);
         store8<true>(out, 8 * c, a_pre[j]);
         if (POST) store8<true>(out, p.W + 8 * c, a_post[j]);
-        if (GATE == GATE_CHANNEL) store8<true>(out, 2 * p.W + 8 * c, a_gate[j]);
+        if (CHANNEL) store8<true>(out, 2 * p.W + 8 * c, a_gate[j]);
     }
 }
 
-// The partial rows of a column added in order: 16 threads a column, 16
-// columns a workgroup, then their 16 sums in order.
+// The partial rows of a column added in a fixed order: 32 columns a workgroup,
+// 8 threads of 4 columns, 32 rows at once and 8 loads in flight a thread, then
+// the 32 sums in order.
 __global__ __launch_bounds__(256) void residual_norm_sum_kernel(const float* partial, int parts, int W, float* dw_pre,
                                                                 float* dw_post, float* dgate)
 {
-    __shared__ float s[16][17];
+    __shared__ float s[32][33];
     float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
     if (!out) return;
-    const int col = threadIdx.x & 15, lane = threadIdx.x >> 4;
-    const int c = blockIdx.x * 16 + col;
-    float v = 0.0f;
-    if (c < W)
-        for (int i = lane; i < parts; i += 16) v += partial[((int64_t)i * 3 + blockIdx.y) * W + c];
-    s[lane][col] = v;
+    const int col = 4 * (threadIdx.x & 7), lane = threadIdx.x >> 3;
+    const int c = blockIdx.x * 32 + col;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < W) {
+        const float* at = partial + (int64_t)blockIdx.y * W + c;
+        for (int i = lane; i < parts; i += 8 * 32) {
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = i + 32 * k < parts ? *reinterpret_cast<const float4*>(at + (int64_t)(i + 32 * k) * 3 * W)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[0] += x[k].x, v[1] += x[k].y, v[2] += x[k].z, v[3] += x[k].w;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[lane][col + k] = v[k];
     __syncthreads();
-    if (lane == 0 && c < W) {
-        v = 0.0f;
-        for (int i = 0; i < 16; ++i) v += s[i][col];
-        out[c] = v;
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < W) {
+        float t = 0.0f;
+        for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+        out[blockIdx.x * 32 + threadIdx.x] = t;
     }
 }
 
-// Vectors a thread, and threads: the fewest vectors that leave at most
-// `most` threads a row.
+// Vectors a thread, and threads a workgroup.
 struct Shape { int vpt, threads; };
 Shape shape_of(int W, int most)
 {
     const int vecs = W / 8;
-    int vpt = vecs <= 64 ? 1 : 2;
-    while (vpt < 4 && (vecs + vpt - 1) / vpt > most) vpt *= 2;
-    const int threads = (vecs + vpt - 1) / vpt;
-    return {vpt, std::max(64, (threads + 63) / 64 * 64)};
+    const int vpt = vecs <= most ? 1 : 2;
+    return {vpt, ((vecs + vpt - 1) / vpt + 63) / 64 * 64};
 }
+constexpr int FWD_SINGLE = 64, BWD_SINGLE = 1024;    // vectors up to which a thread has one
 
 template <bool FWD, int VPT, bool FP32, bool POST, int GATE>
 void launch_one(const NormParams& p, int grid, int threads, hipStream_t stream)
@@ -366,7 +556,8 @@ void launch_one(const NormParams& p, int grid, int threads, hipStream_t stream)
     if constexpr (FWD)
         residual_norm_fwd_kernel<VPT, FP32, POST, GATE><<<grid, threads, 0, stream>>>(p);
     else
-        residual_norm_bwd_kernel<VPT, FP32, POST, GATE><<<grid, threads, 0, stream>>>(p);
+        residual_norm_bwd_kernel<VPT, FP32, POST, GATE><<<
+            grid, threads, ((VPT == 1) + POST + (GATE == GATE_CHANNEL)) * p.W * sizeof(float), stream>>>(p);
 }
 template <bool FWD, int VPT, bool FP32, bool POST>
 void launch_gate(const NormParams& p, int gate, int grid, int threads, hipStream_t stream)
@@ -398,18 +589,25 @@ NormParams params(const NormArgs& a)
 
 } // namespace
 
-// Workgroups of the backward kernel, one partial row each: two a compute
-// unit, more where they are small.
-int residual_norm_parts(int64_t T, int64_t W)
+// The backward kernel's workgroups, one partial row each: one a compute unit,
+// of as many rows at once as 1024 threads hold and the rows give it.
+namespace {
+struct BwdShape { int vpt, row_threads, at_once, grid; };
+BwdShape bwd_shape(int64_t T, int64_t W)
 {
-    const Shape s = shape_of((int)W, 512);
-    return (int)std::min<int64_t>(T, (int64_t)256 * std::max(2, 512 / s.threads));
+    const Shape s = shape_of((int)W, BWD_SINGLE);
+    BwdShape b{s.vpt, s.threads, 1, 0};
+    b.at_once = (int)std::max<int64_t>(1, std::min<int64_t>(1024 / s.threads, T / 256));
+    b.grid = (int)std::min<int64_t>((T + b.at_once - 1) / b.at_once, 256);
+    return b;
 }
+} // namespace
+int residual_norm_parts(int64_t T, int64_t W) { return bwd_shape(T, W).grid; }
 
 hipError_t launch_residual_norm_fwd(const NormArgs& a, hipStream_t stream)
 {
     const NormParams p = params(a);
-    const Shape s = shape_of((int)a.W, 1024);
+    const Shape s = shape_of((int)a.W, FWD_SINGLE);
     const int grid = (int)std::min<int64_t>(a.T, (int64_t)device_cus() * std::max(2, 1536 / s.threads));
     if (s.vpt == 1) launch_types<true, 1>(p, a, grid, s.threads, stream);
     else launch_types<true, 2>(p, a, grid, s.threads, stream);       // 16384 values: 1024 threads
@@ -418,18 +616,17 @@ hipError_t launch_residual_norm_fwd(const NormArgs& a, hipStream_t stream)
 
 hipError_t launch_residual_norm_bwd(const NormArgs& a, hipStream_t stream)
 {
-    const NormParams p = params(a);
-    const Shape s = shape_of((int)a.W, 512);
-    const int grid = residual_norm_parts(a.T, a.W);
-    if (grid > 0) {
-        if (s.vpt == 1) launch_types<false, 1>(p, a, grid, s.threads, stream);
-        else if (s.vpt == 2) launch_types<false, 2>(p, a, grid, s.threads, stream);
-        else launch_types<false, 4>(p, a, grid, s.threads, stream);
+    NormParams p = params(a);
+    const BwdShape s = bwd_shape(a.T, a.W);
+    p.row_threads = s.row_threads;
+    if (s.grid > 0) {
+        if (s.vpt == 1) launch_types<false, 1>(p, a, s.grid, s.row_threads * s.at_once, stream);
+        else launch_types<false, 2>(p, a, s.grid, s.row_threads, stream);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    residual_norm_sum_kernel<<<dim3((unsigned)((a.W + 15) / 16), 3), 256, 0, stream>>>(
-        a.partial, grid, (int)a.W, a.dw_pre, a.w_post ? a.dw_post : nullptr,
+    residual_norm_sum_kernel<<<dim3((unsigned)((a.W + 31) / 32), 3), 256, 0, stream>>>(
+        a.partial, s.grid, (int)a.W, a.dw_pre, a.w_post ? a.dw_post : nullptr,
         a.gate_kind == GATE_CHANNEL ? (float*)a.dgate : nullptr);
     return hipGetLastError();
 }
