@@ -5,8 +5,10 @@ autograd form.
 A pack holds sequences of different lengths one after the other:
 cu_seqlens (int32 [S + 1] on the GPU) says where each begins and ends, and is
 read on the device, so no call waits for the GPU.  attention_fwd and
-attention_bwd keep no state and can be captured into a graph; so can
-attention(), whose backward pass captures like that of any torch function.
+attention_bwd keep no state and can be captured into a graph.  So can
+attention() and its backward pass, once no eager graph of the same leaves is
+alive: torch ties a leaf's gradient to the stream of the graph that holds it,
+and capturing a backward pass beside one ends the process.
 """
 from __future__ import annotations
 
