@@ -45,13 +45,15 @@ struct BwdParams {
     float* ws;            // [H][T] -lse / scale, then [H][T] -delta
     const int32_t* cu;
     int64_t T;
-    int S, H, Hk, tiles, kv_tiles, groups, group_heads, hb;
+    int S, H, hb_shift, group_heads;
+    Order order, kv_order;
+    Divisor share;
     float scale;
 };
 
 constexpr int BN = 64;    // keys a tile of the dq kernel
 constexpr int QN = 64;    // query rows a tile of the dk, dv kernel
-constexpr int KN = 128;   // keys a workgroup of it
+constexpr int KN = 128;   // keys a workgroup of it (1 << 7)
 constexpr int FIRST = 64; // rows at the start of a sequence that are kept more exactly
 static_assert(FIRST == BN && FIRST <= KN && FIRST == QN && KN <= 2 * BN, "one tile of keys, one of queries");
 
@@ -73,14 +75,14 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
     __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rows = 128 / p.hb;
-    const Mine mine = my_tile<false>(p.cu, p.S, p.T, rows, p.tiles, p.groups, lane);
+    const int rows = 128 >> p.hb_shift;
+    const Mine mine = my_tile<false>(p.cu, p.S, p.T, 7 - p.hb_shift, p.order, lane);
     const Where at = mine.at;
     const int group = mine.group;
     const int t0 = at.tile * rows;
     if (t0 >= at.len) return;
-    const int head = group * p.hb + wave % p.hb;
-    const int w0 = t0 + (wave / p.hb) * 32;
+    const int head = (group << p.hb_shift) + (wave & ((1 << p.hb_shift) - 1));
+    const int w0 = t0 + (wave >> p.hb_shift) * 32;
     const int row = w0 + (lane & 31);
     const bool write = row < at.len;
     const int64_t token = at.start + (write ? row : at.len - 1);
@@ -95,7 +97,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
         store_row<D>(dq_row, dq, 0.0f, lane, write);
         return;
     }
-    const int kv_head = head / p.group_heads;
+    const int kv_head = (int)divide(group, p.share);
     const uint16_t* q_row = p.q + token * p.q_ld + head * p.q_hd;
     const uint16_t* do_row = p.dout + token * p.do_ld + head * p.do_hd;
     const uint16_t* o_row = p.o + token * p.o_ld + head * p.o_hd;
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     const int set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
     char* lds = lds_all + set * 2 * STAGE;
-    const Mine mine = my_tile<true>(p.cu, p.S, p.T, KN, p.kv_tiles, p.Hk, lane);
+    const Mine mine = my_tile<true>(p.cu, p.S, p.T, 7, p.kv_order, lane);
     const Where at = mine.at;
     const int kv_head = mine.group;
     const int k0 = at.tile * KN;
@@ -427,15 +429,16 @@ hipError_t launch_attention_bwd(const AttentionArgs& a, hipStream_t stream)
     p.v_ld = a.v.ld_token, p.v_hd = a.v.ld_head, p.o_ld = a.out.ld_token, p.o_hd = a.out.ld_head;
     p.do_ld = a.dout.ld_token, p.do_hd = a.dout.ld_head, p.dq_ld = a.dq.ld_token, p.dq_hd = a.dq.ld_head;
     p.dk_ld = a.dk.ld_token, p.dk_hd = a.dk.ld_head, p.dv_ld = a.dv.ld_token, p.dv_hd = a.dv.ld_head;
-    p.lse = a.lse, p.ws = a.delta, p.cu = a.cu_seqlens, p.T = a.T, p.S = a.S, p.H = a.H, p.Hk = a.Hk;
-    p.group_heads = a.H / a.Hk;
-    p.hb = p.group_heads % 4 == 0 ? 4 : p.group_heads % 2 == 0 ? 2 : 1;
-    p.groups = a.H / p.hb;
-    p.tiles = (int)(a.T / (128 / p.hb)) + a.S + 2;
+    p.lse = a.lse, p.ws = a.delta, p.cu = a.cu_seqlens, p.T = a.T, p.S = a.S, p.H = a.H;
+    const int shared = a.H / a.Hk;
+    p.hb_shift = shared % 4 == 0 ? 2 : shared % 2 == 0 ? 1 : 0;
+    p.group_heads = shared;
+    p.order = Order((int)(a.T / (128 >> p.hb_shift)) + a.S + 2, a.H >> p.hb_shift);
+    p.share = Divisor((uint32_t)(shared >> p.hb_shift));
     p.scale = a.scale;
-    const dim3 grid((unsigned)((int64_t)p.tiles * p.groups));
-    p.kv_tiles = (int)(a.T / KN) + a.S + 2;
-    const dim3 grid_kv((unsigned)((int64_t)p.kv_tiles * a.Hk));
+    const dim3 grid((unsigned)((int64_t)p.order.tiles * p.order.groups));
+    p.kv_order = Order((int)(a.T / KN) + a.S + 2, a.Hk);
+    const dim3 grid_kv((unsigned)((int64_t)p.kv_order.tiles * a.Hk));
     if (a.D == 128) {
         attention_dq_kernel<128><<<grid, 256, 0, stream>>>(p);
         attention_dkv_kernel<128><<<grid_kv, 512, 0, stream>>>(p);

@@ -93,9 +93,6 @@ __device__ __forceinline__ void publish()
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// All waves of the workgroup are here; copies stay in flight.
-__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
-
 // Every load into registers so far has landed, in a form that the compiler
 // sees: before a loop that issues copies, or its waits for those registers
 // inside the loop would wait for the copies as well.
@@ -223,30 +220,30 @@ __device__ __forceinline__ int64_t segment_start(const int32_t* cu, int S, int64
     if (i > S + 1) return T;
     return min(max((int64_t)cu[i - 1], (int64_t)0), T);
 }
-__device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, int rows, int tile, int lane)
-{
+__device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, int shift, int tile, int lane)
+{   // tiles of 1 << shift rows
     // every lane tests one segment: how many start at or before this tile
     Where w;
     int n = 0;
     if (S + 2 < 64) {                   // and keeps its start: one read of cu in all
         const int start = (int)segment_start(cu, S, T, lane);
-        const int seg = __popcll(__ballot(lane < S + 2 && start / rows + lane <= tile)) - 1;
+        const int seg = __popcll(__ballot(lane < S + 2 && (start >> shift) + lane <= tile)) - 1;
         const int a = __builtin_amdgcn_readlane(start, seg), b = __builtin_amdgcn_readlane(start, seg + 1);
         w.start = a;
-        w.tile = tile - (a / rows + seg);
+        w.tile = tile - ((a >> shift) + seg);
         w.len = b > a && w.tile >= 0 ? b - a : 0;
         w.sequence = seg > 0 && seg <= S;
         return w;
     }
     for (int i0 = 0; i0 < S + 2; i0 += 64) {
         const int i = i0 + lane;
-        const bool before = i < S + 2 && (int)(segment_start(cu, S, T, i) / rows) + i <= tile;
+        const bool before = i < S + 2 && (int)(segment_start(cu, S, T, i) >> shift) + i <= tile;
         n += __popcll(__ballot(before));
     }
     const int seg = __builtin_amdgcn_readfirstlane(n - 1);
     const int64_t a = segment_start(cu, S, T, seg), b = segment_start(cu, S, T, seg + 1);
     w.start = __builtin_amdgcn_readfirstlane((int)a);
-    w.tile = __builtin_amdgcn_readfirstlane(tile - ((int)(a / rows) + seg));
+    w.tile = __builtin_amdgcn_readfirstlane(tile - ((int)(a >> shift) + seg));
     w.len = __builtin_amdgcn_readfirstlane(b > a && w.tile >= 0 ? (int)(b - a) : 0);
     w.sequence = seg > 0 && seg <= S;
     return w;
@@ -274,7 +271,7 @@ __device__ __forceinline__ int wave_total(int v)
 // are read once.
 constexpr int SORTED = 256;
 template <bool KEYS>
-__device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int64_t T, int rows, int rank, int lane)
+__device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int64_t T, int shift, int rank, int lane)
 {
     constexpr int C = SORTED / 64;
     int start[C], len[C], n[C], segments = 0;
@@ -286,7 +283,7 @@ __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int
             const int64_t a = segment_start(cu, S, T, i), b = segment_start(cu, S, T, i + 1);
             start[j] = (int)a;
             len[j] = b > a ? (int)(b - a) : 0;
-            n[j] = (int)(((uint32_t)len[j] + rows - 1) / (uint32_t)rows);
+            n[j] = (int)(((uint32_t)len[j] + (1u << shift) - 1) >> shift);
         }
         segments += __popcll(__ballot(n[j] > 0));
     }
@@ -329,27 +326,46 @@ __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int
     return w;
 }
 
-// Workgroup b of a grid of `tiles` x `groups`: its tile and its group of
-// heads.  Workgroups go round the 8 XCDs, each with its own L2: with a
-// multiple of 8 groups, one XCD keeps the same heads.
+// Division of a launch's numbers (below 2^31) by one that the host knows: a
+// product with floor((2^32 - 1) / d) is at most one too small.  A division
+// proper costs a workgroup of a short sequence more than its matrix products.
+struct Divisor {
+    uint32_t d = 1, m = 0xFFFFFFFFu;
+    Divisor() = default;
+    explicit Divisor(uint32_t by) : d(by), m(0xFFFFFFFFu / by) {}
+};
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& by)
+{
+    const uint32_t q = __umulhi(n, by.m);
+    return n - q * by.d >= by.d ? q + 1 : q;
+}
+
+// A grid of `tiles` x `groups` workgroups, the groups of heads innermost.
+// Workgroups go round the 8 XCDs, each with its own L2: with a multiple of 8
+// groups, one XCD keeps the same heads.
+struct Order {
+    int tiles = 0, groups = 1;
+    Divisor by;          // groups / 8 if that is whole, or else groups
+    Order() = default;
+    Order(int tiles_, int groups_)
+        : tiles(tiles_), groups(groups_), by((uint32_t)(groups_ % 8 == 0 ? groups_ / 8 : groups_)) {}
+};
+// This workgroup's tile and its group of heads.
 struct Mine { Where at; int group; };
 template <bool KEYS>
-__device__ __forceinline__ Mine my_tile(const int32_t* cu, int S, int64_t T, int rows, int tiles, int groups, int lane)
+__device__ __forceinline__ Mine my_tile(const int32_t* cu, int S, int64_t T, int shift, const Order& o, int lane)
 {
-    const int b = blockIdx.x;
+    const uint32_t b = blockIdx.x;
+    const bool by_xcd = (o.groups & 7) == 0;
+    const uint32_t x = by_xcd ? b >> 3 : b;
+    const int rank = (int)divide(x, o.by);
+    const int in = (int)(x - rank * o.by.d);
     Mine m;
-    int rank;
-    if (groups % 8 == 0) {
-        m.group = (b & 7) * (groups / 8) + (b >> 3) % (groups / 8);
-        rank = (b >> 3) / (groups / 8);
-    } else {
-        m.group = b % groups;
-        rank = b / groups;
-    }
+    m.group = by_xcd ? (int)((b & 7) * o.by.d) + in : in;
     // queries go by their place: by size, neighbours come from different
     // sequences and share no keys (61 prompts: 46.0 -> 49.2 us)
-    if (KEYS && S + 2 <= SORTED) m.at = find_tile_by_size<KEYS>(cu, S, T, rows, rank, lane);
-    else m.at = find_tile(cu, S, T, rows, KEYS ? rank : tiles - 1 - rank, lane);
+    if (KEYS && S + 2 <= SORTED) m.at = find_tile_by_size<KEYS>(cu, S, T, shift, rank, lane);
+    else m.at = find_tile(cu, S, T, shift, KEYS ? rank : o.tiles - 1 - rank, lane);
     return m;
 }
 

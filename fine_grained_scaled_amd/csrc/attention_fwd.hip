@@ -38,7 +38,9 @@ struct FwdParams {
     float* lse;
     const int32_t* cu;
     int64_t T;
-    int S, tiles, groups, group_heads, hb;   // groups: workgroups a token tile; hb: query heads a workgroup
+    int S, hb_shift;     // 1 << hb_shift query heads a workgroup
+    Order order;
+    Divisor share;       // groups of heads that share a key head
     float scale;
 };
 
@@ -97,14 +99,14 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    const int rows = 128 / p.hb;
-    const Mine mine = my_tile<false>(p.cu, p.S, p.T, rows, p.tiles, p.groups, lane);
+    const int rows = 128 >> p.hb_shift;
+    const Mine mine = my_tile<false>(p.cu, p.S, p.T, 7 - p.hb_shift, p.order, lane);
     const Where at = mine.at;
     const int group = mine.group;
     const int t0 = at.tile * rows;
     if (t0 >= at.len) return;
-    const int head = group * p.hb + wave % p.hb;
-    const int w0 = t0 + (wave / p.hb) * 32;          // the wave's first token in the segment
+    const int head = (group << p.hb_shift) + (wave & ((1 << p.hb_shift) - 1));
+    const int w0 = t0 + (wave >> p.hb_shift) * 32;          // the wave's first token in the segment
     const int row = w0 + (lane & 31);
     const bool write = row < at.len;
     const int64_t token = at.start + (write ? row : at.len - 1);
@@ -122,7 +124,7 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
         return;
     }
 
-    const int kv_head = head / p.group_heads;
+    const int kv_head = (int)divide(group, p.share);
     const uint16_t* q_row = p.q + token * p.q_ld + head * p.q_hd;
     const uint16_t* k_seq = uniform_ptr(p.k + at.start * p.k_ld + kv_head * p.k_hd);
     const uint16_t* v_seq = uniform_ptr(p.v + at.start * p.v_ld + kv_head * p.v_hd);
@@ -307,12 +309,12 @@ hipError_t launch_attention_fwd(const AttentionArgs& a, hipStream_t stream)
     p.q_ld = a.q.ld_token, p.q_hd = a.q.ld_head, p.k_ld = a.k.ld_token, p.k_hd = a.k.ld_head;
     p.v_ld = a.v.ld_token, p.v_hd = a.v.ld_head, p.o_ld = a.out.ld_token, p.o_hd = a.out.ld_head;
     p.lse = a.lse, p.cu = a.cu_seqlens, p.T = a.T, p.S = a.S;
-    p.group_heads = a.H / a.Hk;
-    p.hb = p.group_heads % 4 == 0 ? 4 : p.group_heads % 2 == 0 ? 2 : 1;
-    p.groups = a.H / p.hb;
-    p.tiles = (int)(a.T / (128 / p.hb)) + a.S + 2;
+    const int shared = a.H / a.Hk;
+    p.hb_shift = shared % 4 == 0 ? 2 : shared % 2 == 0 ? 1 : 0;
+    p.order = Order((int)(a.T / (128 >> p.hb_shift)) + a.S + 2, a.H >> p.hb_shift);
+    p.share = Divisor((uint32_t)(shared >> p.hb_shift));
     p.scale = a.scale;
-    const dim3 grid((unsigned)((int64_t)p.tiles * p.groups));
+    const dim3 grid((unsigned)((int64_t)p.order.tiles * p.order.groups));
     if (a.D == 128)
         attention_fwd_kernel<128><<<grid, 256, 0, stream>>>(p);
     else
