@@ -13,17 +13,18 @@
 // A row's p is about 1 / (its keys), so the first rows of a sequence weigh
 // most in every gradient, and there dout . v - delta cancels: row 0 has
 // ds = 0.  The rows that see one tile of keys (the first 64) therefore take
-// delta from their own p and dout . v instead of the rounded out, and hand
-// p and ds to the products as two BF16 terms, value and remainder.  That is
-// one more set of products in one tile of a sequence, and it takes the error
-// of dq, dk and dv against 64 bits from 1.5 to 1.3 times that of the results'
-// own rounding.
+// delta from their own p and dout . v instead of the rounded out, and they
+// (for dk and dv the first 32) hand p and ds to the products as two BF16
+// terms, value and remainder.  That is one more set of products in one tile of
+// a sequence, and it takes the error of dq, dk and dv against 64 bits from 1.5
+// to 1.3 times that of the results' own rounding.
 //
 // Two kernels, each with its sums in registers: one owns query rows (dq, and
 // delta), the other owns keys (dk, dv) and walks the query heads of their
 // group.  They compute the scores twice, 14 D operations a pair instead of
 // 10, and in return no sum crosses workgroups: no atomics, no FP32 copy of
 // dq, and the same bits on every run.
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_device.h"
@@ -48,14 +49,19 @@ struct BwdParams {
     int S, H, hb_shift, group_heads;
     Order order, kv_order;
     Divisor share;
+    Split split;
+    float* shares;        // split key tiles: [slot][dk, dv][4 waves][32 keys x D]
+    int* arrived;         // [slot]: the parts that are done, at the tile's first slot
+    int slots, kv_slots;  // of all heads, of one
     float scale;
 };
 
 constexpr int BN = 64;    // keys a tile of the dq kernel
 constexpr int QN = 64;    // query rows a tile of the dk, dv kernel
 constexpr int KN = 128;   // keys a workgroup of it (1 << 7)
-constexpr int FIRST = 64; // rows at the start of a sequence that are kept more exactly
-static_assert(FIRST == BN && FIRST <= KN && FIRST == QN && KN <= 2 * BN, "one tile of keys, one of queries");
+constexpr int FIRST = 64; // rows at the start of a sequence that are kept more exactly,
+constexpr int REST = 32;  // and those whose remainders go into dk and dv
+static_assert(FIRST == BN && KN <= 2 * BN && REST == 32, "one tile of keys, 32 queries");
 
 // What pack8() drops, rounded in turn.
 __device__ __forceinline__ bf16x8 pack8_rest(const f32x16& s, int i0)
@@ -75,8 +81,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
     __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.slots; i += blockDim.x) p.arrived[i] = 0;
     const int rows = 128 >> p.hb_shift;
-    const Mine mine = my_tile<false>(p.cu, p.S, p.T, 7 - p.hb_shift, p.order, lane);
+    const Mine mine = my_queries(p.cu, p.S, p.T, 7 - p.hb_shift, p.order, lane);
     const Where at = mine.at;
     const int group = mine.group;
     const int t0 = at.tile * rows;
@@ -231,7 +239,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     const int set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
     char* lds = lds_all + set * 2 * STAGE;
-    const Mine mine = my_tile<true>(p.cu, p.S, p.T, 7, p.kv_order, lane);
+    const Mine mine = my_keys(p.cu, p.S, p.T, 7, p.kv_order, p.split, lane);
     const Where at = mine.at;
     const int kv_head = mine.group;
     const int k0 = at.tile * KN;
@@ -266,10 +274,16 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     const uint32_t base = lds_offset(lds);
     const int last = at.len - 1;
     const int q_first = k0 / QN, q_tiles = (at.len + QN - 1) / QN - q_first;
-    const int steps = q_tiles * p.group_heads;
+    // this part's steps: heads of the group and query tiles within them
+    const int all_tiles = q_tiles * p.group_heads;
+    int begin = 0, steps = all_tiles;
+    if (at.parts > 1) {
+        begin = (int)((int64_t)all_tiles * at.part / at.parts);
+        steps = (int)((int64_t)all_tiles * (at.part + 1) / at.parts) - begin;
+    }
     const float c = p.scale * LOG2E;
     // the head and the query tile of the set's step
-    int head = kv_head * p.group_heads, q_index = set;
+    int head = kv_head * p.group_heads + begin / q_tiles, q_index = begin % q_tiles + set;
     auto forward = [&](int& h, int& i) {
         while (i >= q_tiles) i -= q_tiles, ++h;
     };
@@ -361,33 +375,28 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     const int set_steps = (steps + 1 - set) / 2, all_steps = (steps + 1) / 2;
     if (set_steps > 0) load(head, q_index, 0);
     registers_landed();
-    for (int m = 0; m < all_steps; ++m) {
-        publish();
-        const int q0 = (q_first + q_index) * QN;
-        q_index += 2;
-        forward(head, q_index);
-        if (m + 1 < set_steps) load(head, q_index, (m + 1) & 1);
-        if (m >= set_steps) continue;
-        const uint32_t tile = base + (m & 1) * STAGE;
-        const float* row_value = reinterpret_cast<const float*>(lds + (m & 1) * STAGE + 2 * TILE) + 4 * half;
+    // The first key tile of a sequence adds the first rows' remainders, in a
+    // loop of its own: the choice alone cost the other one 10%.
+    auto walk = [&](auto first_tile) {
+        for (int m = 0; m < all_steps; ++m) {
+            publish();
+            const int q0 = (q_first + q_index) * QN;
+            q_index += 2;
+            forward(head, q_index);
+            if (m + 1 < set_steps) load(head, q_index, (m + 1) & 1);
+            if (m >= set_steps) continue;
+            const uint32_t tile = base + (m & 1) * STAGE;
+            const float* row_value = reinterpret_cast<const float*>(lds + (m & 1) * STAGE + 2 * TILE) + 4 * half;
+            if constexpr (decltype(first_tile)::value)
+                if (q0 < REST && w0 < REST) step(std::true_type{}, tile, row_value, q0);
 #pragma unroll
-        for (int t = 0; t < QN / 32; ++t)
-            if (q0 + 32 * t + 31 >= w0 && q0 + 32 * t < at.len)
-                step(std::false_type{}, tile + 32 * t * (D * 2), row_value + 32 * t, q0 + 32 * t);
-    }
-    // the first rows' remainders, head after head; not in the loop above,
-    // where the choice alone cost 10%
-    for (int h = set; k0 < FIRST && h < p.group_heads + set; h += 2) {
-        publish();
-        if (h < p.group_heads) load(kv_head * p.group_heads + h, 0, 0);
-        publish();
-        if (h >= p.group_heads) continue;
-        const float* row_value = reinterpret_cast<const float*>(lds + 2 * TILE) + 4 * half;
-#pragma unroll 1
-        for (int q0 = 0; q0 < FIRST; q0 += 32)
-            if (q0 + 31 >= w0 && q0 < at.len)
-                step(std::true_type{}, base + q0 * (D * 2), row_value + q0, q0);
-    }
+            for (int t = 0; t < QN / 32; ++t)
+                if (q0 + 32 * t + 31 >= w0 && q0 + 32 * t < at.len)
+                    step(std::false_type{}, tile + 32 * t * (D * 2), row_value + 32 * t, q0 + 32 * t);
+        }
+    };
+    if (k0 < REST) walk(std::true_type{});
+    else walk(std::false_type{});
     // the second set's sums, 32 keys x D of FP32 a wave, dk and then dv
     static_assert(4 * 32 * D * 4 <= 4 * STAGE, "the exchange fits");
     f32x4* swap = reinterpret_cast<f32x4*>(lds_all) + wave * (32 * D / 4) + lane;
@@ -413,6 +422,54 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
                     for (int j = 0; j < 4; ++j) acc[dt][4 * g + j] += o[j];
                 }
     }
+    if (at.parts > 1) {
+        // The parts' sums meet in memory: each writes its own, the last one to
+        // arrive adds them in the parts' order, so the bits do not depend on
+        // which one that is.  Nothing waits for another workgroup.  Stores and
+        // loads go past the L2 of their XCD one by one; a fence instead would
+        // write all of it back (2048 tokens, 16 heads of 64: +40 us).
+        constexpr int PER_WAVE = 32 * D / 2, PER_SLOT = 2 * 4 * PER_WAVE;      // in pairs
+        const int first = kv_head * p.kv_slots + at.slot - at.part;
+        uint64_t* mine = reinterpret_cast<uint64_t*>(p.shares) + (int64_t)(first + at.part) * PER_SLOT +
+                         wave * PER_WAVE + lane;
+        if (!set)
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const f32x16& acc = pass ? dv[dt] : dk[dt];
+                        const uint64_t x = (uint64_t)as_u32(acc[2 * g + 1]) << 32 | as_u32(acc[2 * g]);
+                        __hip_atomic_store(mine + pass * 4 * PER_WAVE + 64 * (8 * dt + g), x, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+                    }
+        publish();                             // every wave's stores are done
+        int* ticket = reinterpret_cast<int*>(lds_all);
+        if (threadIdx.x == 0)
+            *ticket = __hip_atomic_fetch_add(p.arrived + first, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        publish();
+        if (set || *ticket != at.parts - 1) return;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
+        const uint64_t* from = mine - (int64_t)at.part * PER_SLOT;
+#pragma unroll 1
+        for (int part = 0; part < at.parts; ++part, from += PER_SLOT)
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const uint64_t x = __hip_atomic_load(from + pass * 4 * PER_WAVE + 64 * (8 * dt + g),
+                                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                        f32x16& acc = pass ? dv[dt] : dk[dt];
+                        acc[2 * g] += as_f32((uint32_t)x);
+                        acc[2 * g + 1] += as_f32((uint32_t)(x >> 32));
+                    }
+    }
     if (set || w0 >= at.len) return;
     store();
 }
@@ -437,7 +494,15 @@ hipError_t launch_attention_bwd(const AttentionArgs& a, hipStream_t stream)
     p.share = Divisor((uint32_t)(shared >> p.hb_shift));
     p.scale = a.scale;
     const dim3 grid((unsigned)((int64_t)p.order.tiles * p.order.groups));
-    p.kv_order = Order((int)(a.T / KN) + a.S + 2, a.Hk);
+    // at most `extra` workgroups a head beyond one a tile, so at most 2 extra
+    // of split tiles (each has two at least)
+    p.split.extra = a.T >= ATTENTION_SPLIT_TOKENS ? ATTENTION_SLOTS / 2 / a.Hk : 0;
+    p.split.least = std::max(1, 8 / shared);
+    p.split.fair = (float)a.Hk / (float)device_cus();
+    p.kv_slots = 2 * p.split.extra;
+    p.slots = p.kv_slots * a.Hk;
+    p.shares = a.shares, p.arrived = a.arrived;
+    p.kv_order = Order((int)(a.T / KN) + a.S + 2 + p.split.extra, a.Hk);
     const dim3 grid_kv((unsigned)((int64_t)p.kv_order.tiles * a.Hk));
     if (a.D == 128) {
         attention_dq_kernel<128><<<grid, 256, 0, stream>>>(p);

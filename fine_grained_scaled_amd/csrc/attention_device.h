@@ -213,6 +213,7 @@ struct Where {
     int len;         // its tokens
     int tile;        // this workgroup's tile within it
     bool sequence;   // a sequence, not what lies outside all of them
+    int part = 0, parts = 1, slot = 0;   // its share of the tile's work, and the share's number
 };
 __device__ __forceinline__ int64_t segment_start(const int32_t* cu, int S, int64_t T, int i)
 {
@@ -262,19 +263,42 @@ __device__ __forceinline__ int wave_total(int v)
     return __builtin_amdgcn_readfirstlane((int)(b[0] + b[1]));
 }
 
-// The same tiles by the work they stand for, most first: a tile that is the
-// m-th of its segment counted from the cheap end (the first query tile sees
-// the fewest keys, the last key tile is seen by the fewest queries) has size
-// m, and workgroup `rank` takes the rank-th tile in order of falling size, so
-// that the longest workgroups start first and the shortest fill the end.
-// Up to SORTED - 2 sequences; each lane holds a few segments, whose bounds
-// are read once.
+__device__ __forceinline__ float wave_total(float v)
+{
+    auto add = [&](int moved) { v += as_f32((uint32_t)moved); };
+    add(__builtin_amdgcn_update_dpp(0, (int)as_u32(v), DPP_XOR1, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, (int)as_u32(v), DPP_XOR2, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, (int)as_u32(v), DPP_HALF_MIRROR, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, (int)as_u32(v), DPP_MIRROR, 0xF, 0xF, false));
+    const auto a = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
+    v = as_f32(a[0]) + as_f32(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
+    return as_f32(__builtin_amdgcn_readfirstlane((int)as_u32(as_f32(b[0]) + as_f32(b[1]))));
+}
+
+// Key tiles that are larger than a compute unit's fair share of the work are
+// cut into parts, so that a long sequence among short ones, or one key head,
+// does not leave a few workgroups running at the end.
+struct Split {
+    int extra;        // workgroups a head that the launch has beyond one a tile; 0: no parts
+    int least;        // tiles up to this size stay whole
+    float fair;       // heads / compute units
+};
+constexpr int MOST_PARTS = 8;
+
+// The key tiles by the work they stand for, most first: the m-th tile from
+// the end of its segment is seen by the m last tiles' queries and has size m,
+// and workgroup `rank` takes the rank-th tile (or part) in order of falling
+// size, so that the longest workgroups start first and the shortest fill the
+// end.  Up to SORTED - 2 sequences; each lane holds a few segments, whose
+// bounds are read once.
 constexpr int SORTED = 256;
-template <bool KEYS>
-__device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int64_t T, int shift, int rank, int lane)
+__device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int64_t T, int shift, const Split& split,
+                                                   int rank, int lane)
 {
     constexpr int C = SORTED / 64;
     int start[C], len[C], n[C], segments = 0;
+    float work = 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const int i = 64 * j + lane;
@@ -284,6 +308,7 @@ __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int
             start[j] = (int)a;
             len[j] = b > a ? (int)(b - a) : 0;
             n[j] = (int)(((uint32_t)len[j] + (1u << shift) - 1) >> shift);
+            if (i > 0 && i <= S) work += 0.5f * (float)n[j] * (float)(n[j] + 1);
         }
         segments += __popcll(__ballot(n[j] > 0));
     }
@@ -293,21 +318,44 @@ __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int
         for (int j = 0; j < C; ++j) v += max(n[j] - m, 0);
         return wave_total(v);
     };
+    int most = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) most = max(most, n[j]);
+    most = (int)__builtin_amdgcn_readfirstlane(max_xor32(max_xor16(max_lanes16((uint32_t)most))));
+    int whole = most, cut = 0, parts = 1;      // sizes above `whole` are cut, `cut` tiles of them
+    if (split.extra > 0) {
+        const int fair = max(split.least, (int)ceilf(fminf(wave_total(work) * split.fair, 1e9f)));
+        if (most > fair) {
+            cut = max(larger(fair), 1);
+            parts = min(min(max((most + fair / 2) / fair, 2), MOST_PARTS), 1 + split.extra / cut);
+            whole = fair;
+        }
+    }
+    auto above = [&](int m) {           // workgroups for the tiles of a size above m
+        const int v = larger(m);
+        return v + (parts - 1) * (m < whole ? cut : v);
+    };
     Where w{0, 0, 0, false};
-    const int all = larger(0);
+    const int all = above(0);
     if (rank >= all) return w;
     int size, r = 0;
-    if (segments == 1) {
+    if (segments == 1 && parts == 1) {
         size = all - rank;              // one sequence: its tiles in order
     } else {
-        int lo = 1, hi = all;           // the smallest size with at most `rank` larger tiles
+        int lo = 1, hi = most;          // the smallest size with at most `rank` workgroups above it
         while (lo < hi) {
             const int m = (lo + hi) / 2;
-            if (larger(m) <= rank) hi = m;
+            if (above(m) <= rank) hi = m;
             else lo = m + 1;
         }
         size = lo;
-        r = rank - larger(size);
+        r = rank - above(size);
+        if (size > whole) {
+            w.parts = parts;
+            w.part = r % parts;
+            w.slot = rank;
+            r /= parts;
+        }
     }
 #pragma unroll
     for (int j = 0; j < C; ++j) {       // the r-th segment that has a tile of this size
@@ -318,7 +366,7 @@ __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int
             const int at = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
             w.start = __builtin_amdgcn_readlane(start[j], at);
             w.len = __builtin_amdgcn_readlane(len[j], at);
-            w.tile = KEYS ? __builtin_amdgcn_readlane(n[j], at) - size : size - 1;
+            w.tile = __builtin_amdgcn_readlane(n[j], at) - size;
             w.sequence = 64 * j + at > 0 && 64 * j + at <= S;
         }
         r -= c;
@@ -352,21 +400,29 @@ struct Order {
 };
 // This workgroup's tile and its group of heads.
 struct Mine { Where at; int group; };
-template <bool KEYS>
-__device__ __forceinline__ Mine my_tile(const int32_t* cu, int S, int64_t T, int shift, const Order& o, int lane)
+struct Place { int rank, group; };
+__device__ __forceinline__ Place my_place(const Order& o)
 {
     const uint32_t b = blockIdx.x;
     const bool by_xcd = (o.groups & 7) == 0;
     const uint32_t x = by_xcd ? b >> 3 : b;
     const int rank = (int)divide(x, o.by);
     const int in = (int)(x - rank * o.by.d);
-    Mine m;
-    m.group = by_xcd ? (int)((b & 7) * o.by.d) + in : in;
-    // queries go by their place: by size, neighbours come from different
-    // sequences and share no keys (61 prompts: 46.0 -> 49.2 us)
-    if (KEYS && S + 2 <= SORTED) m.at = find_tile_by_size<KEYS>(cu, S, T, shift, rank, lane);
-    else m.at = find_tile(cu, S, T, shift, KEYS ? rank : o.tiles - 1 - rank, lane);
-    return m;
+    return {rank, by_xcd ? (int)((b & 7) * o.by.d) + in : in};
+}
+// Query tiles go by their place, the last ones first: by size, neighbours
+// come from different sequences and share no keys (61 prompts: 46.0 -> 49.2 us).
+__device__ __forceinline__ Mine my_queries(const int32_t* cu, int S, int64_t T, int shift, const Order& o, int lane)
+{
+    const Place p = my_place(o);
+    return {find_tile(cu, S, T, shift, o.tiles - 1 - p.rank, lane), p.group};
+}
+__device__ __forceinline__ Mine my_keys(const int32_t* cu, int S, int64_t T, int shift, const Order& o,
+                                        const Split& split, int lane)
+{
+    const Place p = my_place(o);
+    if (S + 2 <= SORTED) return {find_tile_by_size(cu, S, T, shift, split, p.rank, lane), p.group};
+    return {find_tile(cu, S, T, shift, p.rank, lane), p.group};
 }
 
 } // namespace attn

@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     const int rows = 128 >> p.hb_shift;
-    const Mine mine = my_tile<false>(p.cu, p.S, p.T, 7 - p.hb_shift, p.order, lane);
+    const Mine mine = my_queries(p.cu, p.S, p.T, 7 - p.hb_shift, p.order, lane);
     const Where at = mine.at;
     const int group = mine.group;
     const int t0 = at.tile * rows;

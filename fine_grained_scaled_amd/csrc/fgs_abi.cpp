@@ -571,7 +571,7 @@ static int check_attention(const int32_t* cu, int32_t S, int64_t T, int32_t H, i
     if (T == 0) return FGS_OK;
     if (!cu || !aligned(cu, 4)) return fail(FGS_ERR_INVALID_ARG, "cu_seqlens must be a 4-byte aligned device pointer");
     if (T > 0x7FFFFFFF - 256) return fail(FGS_ERR_UNSUPPORTED, "tokens too large (%lld)", (long long)T);
-    if (S > (1 << 24) || (T / 32 + S + 2) * H > 0x7FFFFFFF) return fail(FGS_ERR_UNSUPPORTED, "too many tiles");
+    if (S > (1 << 24) || (T / 32 + S + 2 + fgs::ATTENTION_SLOTS) * H > 0x7FFFFFFF) return fail(FGS_ERR_UNSUPPORTED, "too many tiles");
     return FGS_OK;
 }
 
@@ -597,7 +597,9 @@ int fgs_attention_fwd(const fgs_heads* q, const fgs_heads* k, const fgs_heads* v
 size_t fgs_attention_workspace_bytes(int64_t tokens, int32_t heads)
 {
     if (tokens < 0 || heads < 0) return 0;
-    return (size_t)tokens * heads * 8;
+    const size_t rows = (size_t)tokens * heads * 8;
+    if (tokens < fgs::ATTENTION_SPLIT_TOKENS) return rows;
+    return (rows + 15) / 16 * 16 + fgs::ATTENTION_SLOTS * (fgs::ATTENTION_SLOT_BYTES + sizeof(int));
 }
 
 int fgs_attention_bwd(const fgs_heads* dout, const fgs_heads* q, const fgs_heads* k, const fgs_heads* v,
@@ -625,6 +627,11 @@ int fgs_attention_bwd(const fgs_heads* dout, const fgs_heads* q, const fgs_heads
     fgs::AttentionArgs a{};
     a.q = *q, a.k = *k, a.v = *v, a.out = *out, a.dout = *dout, a.dq = *dq, a.dk = *dk, a.dv = *dv;
     a.lse = const_cast<float*>(lse), a.delta = static_cast<float*>(workspace), a.cu_seqlens = cu_seqlens;
+    if (tokens >= fgs::ATTENTION_SPLIT_TOKENS) {
+        char* at = static_cast<char*>(workspace) + ((size_t)tokens * heads * 8 + 15) / 16 * 16;
+        a.shares = reinterpret_cast<float*>(at);
+        a.arrived = reinterpret_cast<int*>(at + fgs::ATTENTION_SLOTS * fgs::ATTENTION_SLOT_BYTES);
+    }
     a.T = tokens, a.S = num_seqs, a.H = heads, a.Hk = kv_heads, a.D = head_dim, a.scale = scale;
     return hip_status(fgs::launch_attention_bwd(a, static_cast<hipStream_t>(stream)), "attention_bwd launch");
 }

@@ -110,12 +110,16 @@ struct GemmArgs {
 struct AttentionArgs {
     fgs_heads q, k, v, out, dout, dq, dk, dv;   // the backward call uses all, the forward one the first four
     float* lse;                     // [H][T]
-    float* delta;                   // backward workspace [H][T]
+    float* delta;                   // backward workspace: two rows of T a head,
+    float* shares;                  // ATTENTION_SLOTS sums of 128 keys x 2 x 128 values,
+    int* arrived;                   // and as many counters (both from ATTENTION_SPLIT_TOKENS tokens on)
     const int32_t* cu_seqlens;      // device int32 [S + 1]
     int64_t T;
     int32_t S, H, Hk, D;
     float scale;
 };
+constexpr int ATTENTION_SLOTS = 512, ATTENTION_SPLIT_TOKENS = 1024;
+constexpr size_t ATTENTION_SLOT_BYTES = 2 * 128 * 128 * sizeof(float);
 hipError_t launch_attention_fwd(const AttentionArgs& a, hipStream_t stream);
 hipError_t launch_attention_bwd(const AttentionArgs& a, hipStream_t stream);
 

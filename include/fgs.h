@@ -573,8 +573,9 @@ int fgs_attention_bwd(const fgs_heads *dout, const fgs_heads *q, const fgs_heads
                       const fgs_heads *dq, const fgs_heads *dk, const fgs_heads *dv,
                       void *workspace, size_t workspace_bytes, void *stream);
 
-/* Device workspace of fgs_attention_bwd: two FP32 values a head and token
- * (0 for negative arguments). */
+/* Device workspace of fgs_attention_bwd: two FP32 values a head and token, and
+ * from 1024 tokens on 64 MiB more, where the workgroups that share the keys of
+ * a long sequence add their sums (0 for negative arguments). */
 size_t fgs_attention_workspace_bytes(int64_t tokens, int32_t heads);
 
 /*

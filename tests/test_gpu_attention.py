@@ -57,6 +57,26 @@ def test_scores_large_and_small(gain, scale, D):
     _check([200, 40], 2, 2, D, seed=3, gain=gain, scale=scale)
 
 
+@pytest.mark.parametrize("lengths,H,Hk,D", [([1500, 60], 2, 1, 128), ([1300], 4, 1, 64), ([70, 1, 1100, 0, 131], 3, 3, 64),
+                                            ([1280, 1280], 8, 2, 128)], ids=str)
+def test_long_sequences_share_their_key_tiles(lengths, H, Hk, D):
+    """Few heads and a long sequence: several workgroups a key tile, whose
+    sums meet in the workspace; the same bits again, and in a replayed graph."""
+    _check(lengths, H, Hk, D, seed=sum(lengths), before=5, after=130)
+    _, on, dout, cu = _inputs(lengths, H, Hk, D, seed=1)
+    cu, dout = cu.cuda(), dout.cuda()
+    out, lse = fgs.attention_fwd(*on, cu)
+    first = fgs.attention_bwd(dout, *on, out, lse, cu)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fgs.attention_bwd(dout, *on, out, lse, cu)
+    for _ in range(4):
+        again = fgs.attention_bwd(dout, *on, out, lse, cu)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(first, again, got))
+
+
 def test_tokens_of_no_sequence():
     host, on, dout, cu = _inputs([40, 0, 70], 4, 2, 128, seed=5, before=37, after=50)
     _check([40, 0, 70], 4, 2, 128, seed=5, before=37, after=50)
