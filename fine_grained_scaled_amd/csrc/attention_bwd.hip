@@ -77,6 +77,99 @@ __device__ __forceinline__ bf16x8 pack8_rest(const f32x16& s, int i0)
     return r;
 }
 
+// Whether a lane's row or key came out non-finite, in both of its halves.
+template <int D>
+__device__ __forceinline__ bool non_finite(const f32x16* acc)
+{
+    float bad = 0.0f;                          // 0 * x is NaN for a non-finite x and 0 otherwise
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad = __builtin_fmaf(0.0f, acc[dt][i], bad);
+    bad += swap_half(bad);
+    return bad != bad;
+}
+// Two rows' product, from the halves that two lanes hold.
+template <int D>
+__device__ __forceinline__ float dot_rows(const uint16_t* a, const uint16_t* b, int half)
+{
+    float dot = 0.0f;
+#pragma unroll 1
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const bf16x8 x = *reinterpret_cast<const bf16x8*>(a + 16 * ks + 8 * half);
+        const bf16x8 y = *reinterpret_cast<const bf16x8*>(b + 16 * ks + 8 * half);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot = __builtin_fmaf((float)x[j], (float)y[j], dot);
+    }
+    return dot + swap_half(dot);
+}
+template <int D>
+__device__ __forceinline__ void add_row(f32x16* acc, float f, const uint16_t* row, int half)
+{
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const bf16x4 x = *reinterpret_cast<const bf16x4*>(row + 32 * dt + 8 * g + 4 * half);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[dt][4 * g + j] = __builtin_fmaf(f, (float)x[j], acc[dt][4 * g + j]);
+        }
+}
+// The wave's rows of dq (or keys of dk and dv) again, one pair at a time and
+// every hidden pair left out, for those that came out non-finite: the tile
+// products multiply a hidden pair's zero with a row of the tile, and 0 * Inf
+// is NaN.
+template <int D>
+__device__ __forceinline__ void dq_by_pair(const BwdParams& p, const uint16_t* q_row, const uint16_t* do_row,
+                                           const uint16_t* k_seq, const uint16_t* v_seq, float from, float delta,
+                                           int row, int keys, int half, f32x16* dq)
+{
+    const float c = p.scale * LOG2E;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
+#pragma unroll 1
+    for (int key = 0; key < keys; ++key) {
+        const uint16_t* k = k_seq + key * p.k_ld;
+        const float z = dot_rows<D>(q_row, k, half), dp = dot_rows<D>(do_row, v_seq + key * p.v_ld, half);
+        if (key <= row) add_row<D>(dq, __builtin_amdgcn_exp2f((z + from) * c) * (dp + delta), k, half);
+    }
+}
+// A call, with the kernel's arguments by their address: inlined, this slow
+// path cost the kernel's loops 7% by what the compiler kept in registers for it.
+typedef const __attribute__((address_space(4))) BwdParams* KernelArgs;
+template <int D>
+__device__ __attribute__((noinline)) void dkv_by_pair(KernelArgs p, int64_t start, int len, int kv_head, int w0, int key,
+                                                      bool redo)
+{
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const float c = p->scale * LOG2E;
+    const int64_t own = start + min(key, len - 1);
+    const uint16_t* k = p->k + own * p->k_ld + kv_head * p->k_hd;
+    const uint16_t* v = p->v + own * p->v_ld + kv_head * p->v_hd;
+    f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
+#pragma unroll 1
+    for (int h = kv_head * p->group_heads; h < (kv_head + 1) * p->group_heads; ++h)
+#pragma unroll 1
+        for (int t = w0; t < len; ++t) {
+            const int64_t token = start + t;
+            const uint16_t* q = p->q + token * p->q_ld + h * p->q_hd;
+            const uint16_t* g = p->dout + token * p->do_ld + h * p->do_hd;
+            const float z = dot_rows<D>(q, k, half), dp = dot_rows<D>(g, v, half);
+            if (t < key) continue;
+            const float pr = __builtin_amdgcn_exp2f((z + p->ws[(int64_t)h * p->T + token]) * c);
+            add_row<D>(dv, pr, g, half);
+            add_row<D>(dk, pr * (dp + p->ws[(int64_t)(p->H + h) * p->T + token]), q, half);
+        }
+    store_row<D>(p->dk + own * p->dk_ld + kv_head * p->dk_hd, dk, p->scale, lane, redo);
+    store_row<D>(p->dv + own * p->dv_ld + kv_head * p->dv_hd, dv, 1.0f, lane, redo);
+}
+
 // dq: 4 waves as in the forward kernel (HB heads x 128 / HB tokens, 32 rows a
 // wave), S^T = K Q^T and dP^T = V dO^T a 32-key step, dQ^T += K^T dS^T.
 template <int D>
@@ -222,7 +315,12 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
         p.ws[head * p.T + token] = from;
         p.ws[(p.H + head) * p.T + token] = delta;
     }
-    store_row<D>(dq_row, dq, p.scale, lane, write);
+    const bool redo = write && non_finite<D>(dq);
+    store_row<D>(dq_row, dq, p.scale, lane, write && !redo);
+    if (__any(redo)) {
+        dq_by_pair<D>(p, q_row, do_row, k_seq, v_seq, from, delta, row, min(w0 + 32, at.len), half, dq);
+        store_row<D>(dq_row, dq, p.scale, lane, redo);
+    }
 }
 
 // dk and dv: 8 waves, two sets of 4 that own the same 4 x 32 keys, whose key
@@ -259,14 +357,14 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
-    auto store = [&] {
+    auto store = [&](bool write) {
         int key_now = key;                     // addresses formed here are not kept in registers until the end
         asm volatile("" : "+v"(key_now));
         const int64_t token = token_of(key_now);
         store_row<D>(p.dk + token * p.dk_ld + kv_head * p.dk_hd, dk, p.scale, lane, write);
         store_row<D>(p.dv + token * p.dv_ld + kv_head * p.dv_hd, dv, 1.0f, lane, write);
     };
-    if (!at.sequence) return store();
+    if (!at.sequence) return store(write);
     const int64_t token = token_of(key);
     const uint16_t* k_row = p.k + token * p.k_ld + kv_head * p.k_hd;
     const uint16_t* v_row = p.v + token * p.v_ld + kv_head * p.v_hd;
@@ -356,7 +454,9 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
             dp[i] *= s[i];
         }
         if (q0 < w0 + 31 || q0 + 32 > at.len) {
-            const int from = key - q0 - 4 * half, to = at.len - q0 - 4 * half;
+            int lane = threadIdx.x & 63;
+            asm volatile("" : "+v"(lane));     // the key's number is not kept in a register for this
+            const int first = 4 * (lane >> 5), from = w0 + (lane & 31) - q0 - first, to = at.len - q0 - first;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (acc_row(i, 0) < from || acc_row(i, 0) >= to) s[i] = dp[i] = 0.0f;
@@ -476,7 +576,10 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
                     }
     }
     if (set || w0 >= at.len) return;
-    store();
+    const bool bad = non_finite<D>(dk), redo = write && (non_finite<D>(dv) || bad);
+    store(write && !redo);
+    if (__any(redo))
+        dkv_by_pair<D>((KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(), at.start, at.len, kv_head, w0, key, redo);
 }
 
 } // namespace

@@ -559,9 +559,11 @@ int fgs_attention_fwd(const fgs_heads *q, const fgs_heads *k, const fgs_heads *v
  * fgs_attention_bwd -- the gradients dq, dk, dv of fgs_attention_fwd from its
  *   inputs, its out and lse, and dout.  dk and dv sum over the query heads
  *   that share a key head.  Tokens of no sequence get zeros.  The sums have a
- *   fixed order (no atomics): the same inputs give the same bits.  NaN or Inf
- *   in one sequence do not reach another; within one they may reach up to 127
- *   neighbouring rows that the mask hides from them.
+ *   fixed order: the same inputs give the same bits.  NaN or Inf reach what the
+ *   formulas make depend on them and nothing else: in a token's q or dout, its
+ *   dq and the dk, dv of the tokens that it sees; in its k or v, the dq of the
+ *   tokens that see it, and what those rows reach.  (Rows that come out
+ *   non-finite are computed again pair by pair, a slow path.)
  * Layouts, cu_seqlens and limits as fgs_attention_fwd.
  * workspace  DEVICE scratch, 16-byte aligned, of at least
  *   fgs_attention_workspace_bytes(tokens, heads) bytes.

@@ -151,6 +151,32 @@ def test_non_finite_values_stay_where_the_mask_puts_them():
         assert t[:70].isfinite().all() and t[220:].isfinite().all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lengths,at,H,Hk", [([70, 150, 20], 170, 4, 2), ([40, 60], 50, 3, 3), ([30, 1300], 1201, 2, 1)],
+                         ids=str)
+@pytest.mark.parametrize("where", ["dout", "q", "k", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_gradients_of_rows_that_see_nothing_non_finite(where, value, lengths, at, H, Hk, D):
+    """One NaN or Inf in token `at`: the gradients that the formulas keep
+    apart from it are those without it."""
+    host, _, dout, cu = _inputs(lengths, H, Hk, D, seed=23)
+    want = attention(*host, cu, D ** -0.5, dout)
+    x = dict(q=host[0].clone(), k=host[1].clone(), v=host[2].clone(), dout=dout.clone())
+    x[where][at, 0, 7] = value
+    q, k, v = (x[n].cuda() for n in "qkv")
+    out, lse = fgs.attention_fwd(q, k, v, cu.cuda())
+    got = dict(zip(("dq", "dk", "dv"), fgs.attention_bwd(x["dout"].cuda(), q, k, v, out, lse, cu.cuda())))
+    begin, end = next((a, b) for a, b in zip(cu[:-1].tolist(), cu[1:].tolist()) if a <= at < b)
+    every = torch.arange(sum(lengths))
+    other = (every < begin) | (every >= end)
+    if where in ("q", "dout"):      # rows other than `at`; keys that `at` does not see
+        keep = dict(dq=every != at, dk=other | (every > at), dv=other | (every > at))
+    else:                           # rows that do not see `at`; keys of other sequences
+        keep = dict(dq=other | (every < at), dk=other, dv=other)
+    for name, rows in keep.items():
+        within(name, got[name][rows.cuda()], [t[rows] for t in want[name]])
+
+
 def test_rows_without_a_finite_score():
     """Keys of -Inf give a first row scores of -Inf only: out 0, lse -Inf."""
     host, _, _, cu = _inputs([40], 2, 1, 64, seed=11)
