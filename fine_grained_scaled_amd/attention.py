@@ -61,8 +61,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     Tokens of no sequence get out = 0 and lse = -inf."""
     views = _heads(q, "q") + _heads(k, "k") + _heads(v, "v")
     T, H, Hk, D, scale = _check(q, k, v, cu_seqlens, softmax_scale)
-    out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    out = q.new_empty(T, H, D)               # half of what torch.empty takes
+    lse = q.new_empty(H, T, dtype=torch.float32)
     views = array.array("q", views + (out.data_ptr(), H * D, D))
     at = views.buffer_info()[0]
     _lib.check(_lib.load().fgs_attention_fwd(
@@ -87,11 +87,11 @@ def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     gpu = q.get_device()
     if out.get_device() != gpu or dout.get_device() != gpu or lse.get_device() != gpu:
         raise ValueError("all tensors must be on one GPU")
-    dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k, v))
+    dq, dk, dv = q.new_empty(T, H, D), q.new_empty(T, Hk, D), q.new_empty(T, Hk, D)
     lib = _lib.load()
     need = lib.fgs_attention_workspace_bytes(T, H)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = lse.new_empty(-(-need // 4))
     elif workspace.get_device() != gpu or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the same GPU")
     views = array.array("q", views + (dq.data_ptr(), H * D, D, dk.data_ptr(), Hk * D, D, dv.data_ptr(), Hk * D, D))

@@ -28,41 +28,47 @@ def _at(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _matrix(t: torch.Tensor, name: str, shape, dtype) -> None:
+def _matrix(t: torch.Tensor, name: str, shape, dtype, gpu: int) -> int:
+    """t's row stride."""
     if t.dtype != dtype or t.shape != shape:
         raise TypeError(f"{name} must be a [{shape[0]} x {shape[1]}] {dtype} tensor (got {tuple(t.shape)} {t.dtype})")
-    if t.stride(1) != 1:
+    row, value = t.stride()
+    if value != 1:
         raise ValueError(f"{name} must have unit stride along columns")
+    if t.get_device() != gpu:
+        raise ValueError("all tensors must be on one GPU")
+    return row
 
 
-def _weight(t: Optional[torch.Tensor], name: str, width: int) -> None:
-    if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.numel() != width or not t.is_contiguous()):
+def _weight(t: torch.Tensor, name: str, width: int, gpu: int) -> None:
+    if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != width or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 tensor of {width} values")
+    if t.get_device() != gpu:
+        raise ValueError("all tensors must be on one GPU")
 
 
 def _check(y, x, w_post, gate, w_pre):
-    """Shapes and types of the inputs; returns the gate's kind and row stride."""
+    """Shapes, types and places of the inputs; returns the shape, the GPU, the
+    residual's type, the gate's kind and the row strides of y, x and gate."""
     if y.dim() != 2:
         raise TypeError("y must be a [tokens x width] bfloat16 tensor")
-    shape = y.shape
-    if x.dtype not in _RESIDUAL:
+    shape, kind, gpu = y.shape, x.dtype, y.get_device()
+    if kind not in _RESIDUAL:
         raise TypeError("the residual must be float32 or bfloat16")
-    _matrix(y, "y", shape, torch.bfloat16)
-    _matrix(x, "the residual", shape, x.dtype)
-    _weight(w_pre, "w_pre", shape[1])
-    _weight(w_post, "w_post", shape[1])
-    _need_gpu(y)
-    gpu = y.get_device()
-    for t in (x, w_pre, w_post, gate):
-        if t is not None and t.get_device() != gpu:
-            raise ValueError("all tensors must be on one GPU")
+    ldy = _matrix(y, "y", shape, torch.bfloat16, gpu)
+    width = shape[1]
+    for t, name in ((w_pre, "w_pre"), (w_post, "w_post")):
+        if t is not None:
+            _weight(t, name, width, gpu)
+    if not y.is_cuda:
+        _need_gpu(y)
+    ldx = _matrix(x, "the residual", shape, kind, gpu)
     if gate is None:
-        return _lib.GATE_NONE, 0
+        return shape, gpu, _RESIDUAL[kind], _lib.GATE_NONE, ldy, ldx, 0
     if gate.dim() == 1:
-        _weight(gate, "gate", shape[1])
-        return _lib.GATE_CHANNEL, 0
-    _matrix(gate, "gate", shape, torch.bfloat16)
-    return _lib.GATE_TOKEN, gate.stride(0)
+        _weight(gate, "gate", width, gpu)
+        return shape, gpu, _RESIDUAL[kind], _lib.GATE_CHANNEL, ldy, ldx, 0
+    return shape, gpu, _RESIDUAL[kind], _lib.GATE_TOKEN, ldy, ldx, _matrix(gate, "gate", shape, torch.bfloat16, gpu)
 
 
 def residual_norm_fwd(y: torch.Tensor, x: torch.Tensor, *, w_pre: torch.Tensor, w_post: Optional[torch.Tensor] = None,
@@ -72,13 +78,11 @@ def residual_norm_fwd(y: torch.Tensor, x: torch.Tensor, *, w_pre: torch.Tensor, 
     residual (float32 or bfloat16, r in its type, rounded before it is
     normed), n bfloat16.  w_post None: y is not normed.  gate: None, float32
     [width] or bfloat16 [tokens x width].  Weights are float32 [width]."""
-    kind, ldg = _check(y, x, w_post, gate, w_pre)
-    T, W = y.shape
-    r = torch.empty((T, W), dtype=x.dtype, device=y.device)
-    n = torch.empty((T, W), dtype=torch.bfloat16, device=y.device)
+    (T, W), gpu, residual, kind, ldy, ldx, ldg = _check(y, x, w_post, gate, w_pre)
+    r, n = x.new_empty(T, W), y.new_empty(T, W)      # a call of few rows is bound by this: torch.empty takes twice as long
     _lib.check(_lib.load().fgs_residual_norm_fwd(
-        _at(y), y.stride(0), _at(x), x.stride(0), _RESIDUAL[x.dtype], T, W, _at(w_post), _at(gate), ldg, kind,
-        alpha, _at(w_pre), eps, _at(r), _at(n), _stream_of(y)))
+        y.data_ptr(), ldy, x.data_ptr(), ldx, residual, T, W, _at(w_post), _at(gate), ldg, kind,
+        alpha, w_pre.data_ptr(), eps, r.data_ptr(), n.data_ptr(), _stream_of(y)))
     return r, n
 
 
@@ -90,27 +94,24 @@ def residual_norm_bwd(dr: torch.Tensor, dn: torch.Tensor, y: torch.Tensor, r: to
     channel-gate gradients are float32, the others have their input's type.
     workspace: optional uint8 device scratch of
     fgs_residual_norm_workspace_bytes() bytes."""
-    kind, ldg = _check(y, r, w_post, gate, w_pre)
-    T, W = y.shape
-    _matrix(dr, "dr", y.shape, r.dtype)
-    _matrix(dn, "dn", y.shape, torch.bfloat16)
-    if dr.get_device() != y.get_device() or dn.get_device() != y.get_device():
-        raise ValueError("all tensors must be on one GPU")
-    dev = y.device
-    dx = torch.empty((T, W), dtype=r.dtype, device=dev)
-    dy = torch.empty((T, W), dtype=torch.bfloat16, device=dev)
-    dgate = torch.empty_like(gate, memory_format=torch.contiguous_format) if gate is not None else None
-    dw_post = torch.empty_like(w_post) if w_post is not None else None
-    dw_pre = torch.empty_like(w_pre)
+    shape, gpu, residual, kind, ldy, ldr, ldg = _check(y, r, w_post, gate, w_pre)
+    T, W = shape
+    lddr = _matrix(dr, "dr", shape, r.dtype, gpu)
+    lddn = _matrix(dn, "dn", shape, torch.bfloat16, gpu)
+    dx, dy = r.new_empty(T, W), y.new_empty(T, W)
+    dgate = gate.new_empty(gate.shape) if gate is not None else None
+    dw_post = w_post.new_empty(W) if w_post is not None else None
+    dw_pre = w_pre.new_empty(W)
     lib = _lib.load()
     if workspace is None:
-        workspace = torch.empty(lib.fgs_residual_norm_workspace_bytes(T, W), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = w_pre.new_empty(-(-lib.fgs_residual_norm_workspace_bytes(T, W) // 4))
+    elif workspace.get_device() != gpu or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the same GPU")
     _lib.check(lib.fgs_residual_norm_bwd(
-        _at(dr), dr.stride(0), _at(dn), dn.stride(0), _at(y), y.stride(0), _at(r), r.stride(0), _RESIDUAL[r.dtype],
-        T, W, _at(w_post), _at(gate), ldg, kind, alpha, _at(w_pre), eps, _at(dx), _at(dy), _at(dgate),
-        _at(dw_post), _at(dw_pre), _at(workspace), workspace.numel() * workspace.element_size(), _stream_of(y)))
+        dr.data_ptr(), lddr, dn.data_ptr(), lddn, y.data_ptr(), ldy, r.data_ptr(), ldr, residual,
+        T, W, _at(w_post), _at(gate), ldg, kind, alpha, w_pre.data_ptr(), eps, dx.data_ptr(), dy.data_ptr(), _at(dgate),
+        _at(dw_post), dw_pre.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_of(y)))
     return ResidualNormGrads(dx, dy, dgate, dw_post, dw_pre)
 
 
