@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import fine_grained_scaled_amd as fgs
+from fine_grained_scaled_amd import _lib
 from _operator_refs import residual_norm, residual_norm_grads, within
 
 pytestmark = pytest.mark.gpu
@@ -64,6 +65,43 @@ def test_widths(rows, width):
 @pytest.mark.parametrize("rows,width", [(1100, 64), (2500, 128), (1537, 520), (700, 8192)])
 def test_more_rows_than_workgroups(rows, width):
     _check(*_inputs(rows, width, "fp32", True, "channel", seed=rows))
+
+
+@pytest.mark.parametrize("rows,width,residual,post,gate", [
+    (300, 8200, "fp32", True, "token"), (261, 16384, "fp32", True, "channel"), (300, 16384, "bf16", True, "channel"),
+    (270, 12296, "fp32", False, "channel"), (270, 12296, "bf16", False, "none"), (513, 8208, "fp32", True, "none")])
+def test_wide_rows_more_than_workgroups(rows, width, residual, post, gate):
+    """Rows of two vectors a thread, several to a workgroup."""
+    _check(*_inputs(rows, width, residual, post, gate, seed=rows))
+
+
+# rows held at once by one workgroup, and the first counts that are not
+@pytest.mark.parametrize("rows,width", [(16, 64), (17, 64), (2, 4096), (3, 4096), (512, 136), (4097, 8)])
+def test_rows_at_once(rows, width):
+    _check(*_inputs(rows, width, "bf16", True, "channel", seed=rows))
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_sums_written_to_any_place(rows):
+    """The gradients of weights and channel gate need no alignment beyond
+    their values'."""
+    s, how = _inputs(rows, 64, "fp32", True, "channel", seed=7)
+    dev = {k: t.cuda() for k, t in (s | how).items()}
+    want = fgs.residual_norm_bwd(dev["dr"], dev["dn"], dev["y"], dev["x"], w_pre=dev["w_pre"], w_post=dev["w_post"],
+                                 gate=dev["gate"])
+    lib = _lib.load()
+    sums = torch.full((3, 68), 9.0, device="cuda")
+    dx, dy = torch.empty_like(dev["x"]), torch.empty_like(dev["y"])
+    ws = torch.empty(lib.fgs_residual_norm_workspace_bytes(rows, 64), dtype=torch.uint8, device="cuda")
+    at = lambda t: t.data_ptr()
+    _lib.check(lib.fgs_residual_norm_bwd(
+        at(dev["dr"]), 64, at(dev["dn"]), 64, at(dev["y"]), 64, at(dev["x"]), 64, _lib.OUT_FP32, rows, 64,
+        at(dev["w_post"]), at(dev["gate"]), 0, _lib.GATE_CHANNEL, 1.0, at(dev["w_pre"]), 1e-6, at(dx), at(dy),
+        at(sums[0, 1:]), at(sums[1, 1:]), at(sums[2, 1:]), at(ws), ws.numel(),
+        torch.cuda.current_stream().cuda_stream))
+    for got, name in zip(sums, ("gate", "w_post", "w_pre")):
+        assert torch.equal(got[1:65], getattr(want, name)) and (got[[0, 65, 66, 67]] == 9.0).all()
+    assert torch.equal(dx, want.residual) and torch.equal(dy, want.y)
 
 
 def test_row_strides():
