@@ -350,7 +350,7 @@ __device__ __forceinline__ Where find_tile_by_size(const int32_t* cu, int S, int
         }
         size = lo;
         r = rank - above(size);
-        if (size > whole) {
+        if (size > whole && rank < 2 * split.extra) {      // (always, with offsets that do not decrease)
             w.parts = parts;
             w.part = r % parts;
             w.slot = rank;
