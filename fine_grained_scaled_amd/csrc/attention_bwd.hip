@@ -77,95 +77,155 @@ __device__ __forceinline__ bf16x8 pack8_rest(const f32x16& s, int i0)
     return r;
 }
 
-// Whether a lane's row or key came out non-finite, in both of its halves.
+// The wave's rows of dq again, for those (redo) that came out non-finite though
+// what they see may be finite: the tile products multiply a hidden pair's zero
+// with a row of the tile, and 0 * Inf is NaN.  The keys before the wave's rows,
+// which all of these see, go by tiles as they did, the others, at most 32, one
+// pair at a time and every hidden pair left out, so the cost stays near that of
+// the wave's first pass.  Nothing is done if no NaN or Inf is among the keys of
+// the tiles with hidden pairs.  A call, with the kernel's arguments by their
+// address, so that the kernel's loops keep their registers.
+// `lds`: 2 * 32 rows of D that are the wave's own.
+typedef const __attribute__((address_space(4))) BwdParams* KernelArgs;
 template <int D>
-__device__ __forceinline__ bool non_finite(const f32x16* acc)
+__device__ __attribute__((noinline)) void dq_again(KernelArgs p, int start, int len, int head, int kv_head, int w0,
+                                                   float from, float delta, bool redo, uint32_t lds)
 {
-    float bad = 0.0f;                          // 0 * x is NaN for a non-finite x and 0 otherwise
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) bad = __builtin_fmaf(0.0f, acc[dt][i], bad);
-    bad += swap_half(bad);
-    return bad != bad;
-}
-// Two rows' product, from the halves that two lanes hold.
-template <int D>
-__device__ __forceinline__ float dot_rows(const uint16_t* a, const uint16_t* b, int half)
-{
-    float dot = 0.0f;
-#pragma unroll 1
-    for (int ks = 0; ks < D / 16; ++ks) {
-        const bf16x8 x = *reinterpret_cast<const bf16x8*>(a + 16 * ks + 8 * half);
-        const bf16x8 y = *reinterpret_cast<const bf16x8*>(b + 16 * ks + 8 * half);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dot = __builtin_fmaf((float)x[j], (float)y[j], dot);
-    }
-    return dot + swap_half(dot);
-}
-template <int D>
-__device__ __forceinline__ void add_row(f32x16* acc, float f, const uint16_t* row, int half)
-{
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const bf16x4 x = *reinterpret_cast<const bf16x4*>(row + 32 * dt + 8 * g + 4 * half);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[dt][4 * g + j] = __builtin_fmaf(f, (float)x[j], acc[dt][4 * g + j]);
-        }
-}
-// The wave's rows of dq (or keys of dk and dv) again, one pair at a time and
-// every hidden pair left out, for those that came out non-finite: the tile
-// products multiply a hidden pair's zero with a row of the tile, and 0 * Inf
-// is NaN.
-template <int D>
-__device__ __forceinline__ void dq_by_pair(const BwdParams& p, const uint16_t* q_row, const uint16_t* do_row,
-                                           const uint16_t* k_seq, const uint16_t* v_seq, float from, float delta,
-                                           int row, int keys, int half, f32x16* dq)
-{
-    const float c = p.scale * LOG2E;
+    constexpr int TILE = 32 * D * 2;
+    // the same in every lane, which a call does not tell the compiler
+    start = __builtin_amdgcn_readfirstlane(start), len = __builtin_amdgcn_readfirstlane(len);
+    head = __builtin_amdgcn_readfirstlane(head), kv_head = __builtin_amdgcn_readfirstlane(kv_head);
+    w0 = __builtin_amdgcn_readfirstlane(w0), lds = __builtin_amdgcn_readfirstlane(lds);
+    const int lane = threadIdx.x & 63, half = lane >> 5, last = len - 1, row = min(w0 + (lane & 31), last);
+    const int64_t k_ld = p->k_ld, v_ld = p->v_ld, token = start + row;
+    const uint16_t* k_seq = p->k + start * k_ld + kv_head * p->k_hd;
+    const uint16_t* v_seq = p->v + start * v_ld + kv_head * p->v_hd;
+    if (!rows_non_finite<D, BN>(k_seq, k_ld, w0, last, lane)) return;
+
+    const uint16_t* q_row = p->q + token * p->q_ld + head * p->q_hd;
+    const uint16_t* do_row = p->dout + token * p->do_ld + head * p->do_hd;
+    const float c = p->scale * LOG2E;
+    const uint32_t rows_at = lds + rows_address<D>(lane), tr_at = lds + tr_address<D>(lane);
+    f32x16 dq[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
 #pragma unroll 1
-    for (int key = 0; key < keys; ++key) {
-        const uint16_t* k = k_seq + key * p.k_ld;
-        const float z = dot_rows<D>(q_row, k, half), dp = dot_rows<D>(do_row, v_seq + key * p.v_ld, half);
+    for (int k0 = 0; k0 < w0; k0 += 32) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // the last tile has been read
+        stage<D, 32, 1>(uniform_ptr(k_seq + k0 * k_ld), (uint32_t)k_ld * 2, 31, lds, 0, lane);
+        stage<D, 32, 1>(uniform_ptr(v_seq + k0 * v_ld), (uint32_t)v_ld * 2, 31, lds + TILE, 0, lane);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        f32x16 s, dp;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = from, dp[i] = delta;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            s = mfma(read_rows_at(rows_at, ks, 0), *reinterpret_cast<const bf16x8*>(q_row + 16 * ks + 8 * half), s);
+            dp = mfma(read_rows_at(rows_at, ks, TILE), *reinterpret_cast<const bf16x8*>(do_row + 16 * ks + 8 * half), dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+                dq[dt] = mfma(read_tr_at<D>(tr_at, 16 * ks, dt, 0), pack8(s, 8 * ks), dq[dt]);
+    }
+#pragma unroll 1
+    for (int key = w0; key < min(w0 + 32, len); ++key) {
+        const uint16_t* k = k_seq + key * k_ld;
+        const float z = dot_rows<D>(q_row, k, half), dp = dot_rows<D>(do_row, v_seq + key * v_ld, half);
         if (key <= row) add_row<D>(dq, __builtin_amdgcn_exp2f((z + from) * c) * (dp + delta), k, half);
     }
+    store_row<D>(p->dq + token * p->dq_ld + head * p->dq_hd, dq, p->scale, lane, redo);
 }
-// A call, with the kernel's arguments by their address: inlined, this slow
+
+// The wave's keys of dk and dv again, for those (redo) that came out non-finite
+// though what they see may be finite: the wave's first 32 queries of each head,
+// where pairs are hidden, one pair at a time, all later ones by tiles, which are
+// right as they are.  Nothing is done if no NaN or Inf is among those first
+// queries.  A call, with the kernel's arguments by their address: inlined, this
 // path cost the kernel's loops 7% by what the compiler kept in registers for it.
-typedef const __attribute__((address_space(4))) BwdParams* KernelArgs;
+// `lds`: 2 * 32 rows of D that are the wave's own.
 template <int D>
-__device__ __attribute__((noinline)) void dkv_by_pair(KernelArgs p, int64_t start, int len, int kv_head, int w0, int key,
-                                                      bool redo)
+__device__ __attribute__((noinline)) void dkv_again(KernelArgs p, int start, int len, int kv_head, int w0, bool redo,
+                                                    uint32_t lds)
 {
-    const int lane = threadIdx.x & 63, half = lane >> 5;
+    constexpr int TILE = 32 * D * 2;
+    start = __builtin_amdgcn_readfirstlane(start), len = __builtin_amdgcn_readfirstlane(len);
+    kv_head = __builtin_amdgcn_readfirstlane(kv_head);
+    w0 = __builtin_amdgcn_readfirstlane(w0), lds = __builtin_amdgcn_readfirstlane(lds);
+    const int lane = threadIdx.x & 63, half = lane >> 5, key = w0 + (lane & 31), last = len - 1;
+    const int first_head = kv_head * p->group_heads, heads_end = first_head + p->group_heads;
+    const int64_t q_ld = p->q_ld, do_ld = p->do_ld;
+    bool hidden = false;
+#pragma unroll 1
+    for (int h = first_head; h < heads_end; ++h)
+        hidden |= rows_non_finite<D, 32>(p->q + start * q_ld + h * p->q_hd, q_ld, w0, last, lane) ||
+                  rows_non_finite<D, 32>(p->dout + start * do_ld + h * p->do_hd, do_ld, w0, last, lane);
+    if (!hidden) return;
+
     const float c = p->scale * LOG2E;
-    const int64_t own = start + min(key, len - 1);
-    const uint16_t* k = p->k + own * p->k_ld + kv_head * p->k_hd;
-    const uint16_t* v = p->v + own * p->v_ld + kv_head * p->v_hd;
+    const int64_t own = (int64_t)start + min(key, last);
+    const uint16_t* k_row = p->k + own * p->k_ld + kv_head * p->k_hd;
+    const uint16_t* v_row = p->v + own * p->v_ld + kv_head * p->v_hd;
+    const uint32_t rows_at = lds + rows_address<D>(lane), tr_at = lds + tr_address<D>(lane);
     f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
 #pragma unroll 1
-    for (int h = kv_head * p->group_heads; h < (kv_head + 1) * p->group_heads; ++h)
+    for (int h = first_head; h < heads_end; ++h) {
+        const float* from = p->ws + (int64_t)h * p->T + start;
+        const float* delta = p->ws + (int64_t)(p->H + h) * p->T + start;
+        const uint16_t* q_seq = p->q + start * q_ld + h * p->q_hd;
+        const uint16_t* g_seq = p->dout + start * do_ld + h * p->do_hd;
 #pragma unroll 1
-        for (int t = w0; t < len; ++t) {
-            const int64_t token = start + t;
-            const uint16_t* q = p->q + token * p->q_ld + h * p->q_hd;
-            const uint16_t* g = p->dout + token * p->do_ld + h * p->do_hd;
-            const float z = dot_rows<D>(q, k, half), dp = dot_rows<D>(g, v, half);
+        for (int t = w0; t < min(w0 + 32, len); ++t) {
+            const uint16_t *q = q_seq + t * q_ld, *g = g_seq + t * do_ld;
+            const float z = dot_rows<D>(q, k_row, half), dp = dot_rows<D>(g, v_row, half);
             if (t < key) continue;
-            const float pr = __builtin_amdgcn_exp2f((z + p->ws[(int64_t)h * p->T + token]) * c);
+            const float pr = __builtin_amdgcn_exp2f((z + from[t]) * c);
             add_row<D>(dv, pr, g, half);
-            add_row<D>(dk, pr * (dp + p->ws[(int64_t)(p->H + h) * p->T + token]), q, half);
+            add_row<D>(dk, pr * (dp + delta[t]), q, half);
         }
+#pragma unroll 1
+        for (int q0 = w0 + 32; q0 < len; q0 += 32) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the last tile has been read
+            stage<D, 32, 1>(uniform_ptr(q_seq + q0 * q_ld), (uint32_t)q_ld * 2, last - q0, lds, 0, lane);
+            stage<D, 32, 1>(uniform_ptr(g_seq + q0 * do_ld), (uint32_t)do_ld * 2, last - q0, lds + TILE, 0, lane);
+            f32x16 s, dp;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int t = min(q0 + acc_row(i, half), last);
+                s[i] = from[t], dp[i] = delta[t];
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                s = mfma(read_rows_at(rows_at, ks, 0), *reinterpret_cast<const bf16x8*>(k_row + 16 * ks + 8 * half), s);
+                dp = mfma(read_rows_at(rows_at, ks, TILE), *reinterpret_cast<const bf16x8*>(v_row + 16 * ks + 8 * half),
+                          dp);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = q0 + acc_row(i, half) > last ? 0.0f : __builtin_amdgcn_exp2f(s[i] * c);
+                dp[i] = q0 + acc_row(i, half) > last ? 0.0f : dp[i] * s[i];
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 pr = pack8(s, 8 * ks), ds = pack8(dp, 8 * ks);
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt) {
+                    dv[dt] = mfma(read_tr_at<D>(tr_at, 16 * ks, dt, TILE), pr, dv[dt]);
+                    dk[dt] = mfma(read_tr_at<D>(tr_at, 16 * ks, dt, 0), ds, dk[dt]);
+                }
+            }
+        }
+    }
     store_row<D>(p->dk + own * p->dk_ld + kv_head * p->dk_hd, dk, p->scale, lane, redo);
     store_row<D>(p->dv + own * p->dv_ld + kv_head * p->dv_hd, dv, 1.0f, lane, redo);
 }
@@ -176,7 +236,7 @@ template <int D>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdParams p)
 {
     constexpr int TILE = BN * D * 2;
-    __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
+    __shared__ __attribute__((aligned(256))) char lds[4 * TILE];   // K0 K1 V0 V1
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0)
@@ -274,8 +334,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
             }
         }
     }
-    if (w0 >= at.len) return;
-    if (w0 < FIRST) {                                  // their tile is still in LDS
+    if (w0 < FIRST && w0 < at.len) {                   // their tile is still in LDS
         f32x16 s[2], dp[2];
         float sum = 0.0f;
 #pragma unroll
@@ -311,16 +370,18 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
             }
         }
     }
+    publish();                                 // from here on each wave has a part of the tiles' place to itself
+    if (w0 >= at.len) return;
     if (write && half == 0) {
         p.ws[head * p.T + token] = from;
         p.ws[(p.H + head) * p.T + token] = delta;
     }
     const bool redo = write && non_finite<D>(dq);
-    store_row<D>(dq_row, dq, p.scale, lane, write && !redo);
-    if (__any(redo)) {
-        dq_by_pair<D>(p, q_row, do_row, k_seq, v_seq, from, delta, row, min(w0 + 32, at.len), half, dq);
-        store_row<D>(dq_row, dq, p.scale, lane, redo);
-    }
+    store_row<D>(dq_row, dq, p.scale, lane, write);
+    static_assert(2 * 32 * D * 2 <= TILE, "two tiles of 32 rows");
+    if (__any(redo))
+        dq_again<D>((KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(), (int)at.start, at.len, head, kv_head, w0, from,
+                    delta, redo, base + wave * TILE);
 }
 
 // dk and dv: 8 waves, two sets of 4 that own the same 4 x 32 keys, whose key
@@ -331,9 +392,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_dq_kernel(BwdP
 // of them takes half as long.  S = Q K^T and dP = dO V^T leave a lane one key
 // and 16 queries a step, again the B operands of dV^T += dO^T P and
 // dK^T += Q^T dS; both start from the row's value (-lse / scale, -delta)
-// instead of zero.
+// instead of zero.  With 64-wide heads a third of a SIMD's registers is a wave's
+// limit, dkv_again() included, so that the next workgroup starts when one of
+// this one's sets is done (4099 tokens: 38.0 us with 249 registers, 35.6 so).
 template <int D>
-__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
+__global__ __launch_bounds__(512, D == 64 ? 3 : 2) void attention_dkv_kernel(BwdParams p)
 {
     constexpr int TILE = QN * D * 2;
     constexpr int STAGE = 2 * TILE + 2 * 64 * 4;          // Q, dO, then the row values, 64 a copy
@@ -575,11 +638,15 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(BwdParams p)
                         acc[2 * g + 1] += as_f32((uint32_t)(x >> 32));
                     }
     }
-    if (set || w0 >= at.len) return;
+    if (set) return;
+    publish();                                 // from here on each wave left has a part of the tiles' place to itself
+    if (w0 >= at.len) return;
     const bool bad = non_finite<D>(dk), redo = write && (non_finite<D>(dv) || bad);
-    store(write && !redo);
+    store(write);
+    static_assert(2 * 32 * D * 2 <= STAGE && STAGE % 256 == 0, "two tiles of 32 rows");
     if (__any(redo))
-        dkv_by_pair<D>((KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(), at.start, at.len, kv_head, w0, key, redo);
+        dkv_again<D>((KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(), (int)at.start, at.len, kv_head, w0, redo,
+                     lds_offset(lds_all) + wave * STAGE);
 }
 
 } // namespace

@@ -175,6 +175,64 @@ __device__ __forceinline__ bf16x8 read_tr_at(uint32_t address, int r0, int dt, u
     return u.v;
 }
 
+// Two rows' product, from the halves that two lanes hold.
+template <int D>
+__device__ __forceinline__ float dot_rows(const uint16_t* a, const uint16_t* b, int half)
+{
+    float dot = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const bf16x8 x = *reinterpret_cast<const bf16x8*>(a + 16 * ks + 8 * half);
+        const bf16x8 y = *reinterpret_cast<const bf16x8*>(b + 16 * ks + 8 * half);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot = __builtin_fmaf((float)x[j], (float)y[j], dot);
+    }
+    return dot + swap_half(dot);
+}
+// acc += f times a row, the lane's values of it.
+template <int D>
+__device__ __forceinline__ void add_row(f32x16* acc, float f, const uint16_t* row, int half)
+{
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const bf16x4 x = *reinterpret_cast<const bf16x4*>(row + 32 * dt + 8 * g + 4 * half);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[dt][4 * g + j] = __builtin_fmaf(f, (float)x[j], acc[dt][4 * g + j]);
+        }
+}
+
+// Whether a lane's row or key came out non-finite, in both of its halves.
+template <int D>
+__device__ __forceinline__ bool non_finite(const f32x16* acc)
+{
+    float bad = 0.0f;                          // 0 * x is NaN for a non-finite x and 0 otherwise
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad = __builtin_fmaf(0.0f, acc[dt][i], bad);
+    bad += swap_half(bad);
+    return bad != bad;
+}
+// Whether a NaN or Inf is among rows first .. first + ROWS - 1 of `base` (rows
+// past `last` are not read): the largest magnitude of all, as integers.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+template <int D, int ROWS>
+__device__ __forceinline__ bool rows_non_finite(const uint16_t* base, int64_t ld, int first, int last, int lane)
+{
+    u16x2 top = {0, 0};
+#pragma unroll 4
+    for (int j = 0; j < ROWS * D / 512; ++j) {
+        const int row = min(first + (64 * j + lane) / (D / 8), last);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(base + row * ld + 8 * (lane % (D / 8)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+    }
+    return __any(max(top[0], top[1]) >= 0x7F80);
+}
+
 // An accumulator tile set acc[D / 32] (rows: values of the head, column: the
 // lane's row) written as bf16 to one row per lane, times f: the lane halves
 // swap 4-value pieces so that each lane writes 16 bytes.

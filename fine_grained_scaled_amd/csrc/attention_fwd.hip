@@ -50,58 +50,75 @@ struct FwdParams {
     float scale;
 };
 
-// The wave's rows again, one key at a time and every hidden key left out:
-// for rows whose output came out non-finite, because the tile products below
-// multiply a hidden key's zero probability with its value, and 0 * Inf is
-// NaN.  Here a row depends on the keys it sees and on nothing else.
+// The wave's output rows again, for those (redo) that came out non-finite
+// though what they see may be finite: the tile products below multiply a hidden
+// key's zero probability with its value, and 0 * Inf is NaN.  The keys before
+// the wave's rows, which all of these see, go by tiles as they did, with the m
+// and l that the row has; the others, at most 32, one key at a time to the rows
+// that see it.  So a row depends on the keys it sees and on nothing else, and
+// the cost stays near that of the wave's first pass.  Nothing is done if no NaN
+// or Inf is among the values of the wave's last tile, the only one with hidden
+// keys.  A call, with the kernel's arguments by their address, so that the
+// kernel's loop keeps its registers.  `lds`: 2 * 32 rows of D that are the wave's own.
+typedef const __attribute__((address_space(4))) FwdParams* KernelArgs;
 template <int D>
-__device__ __forceinline__ void rows_by_key(const FwdParams& p, const uint16_t* q_row, const uint16_t* k_seq,
-                                         const uint16_t* v_seq, uint16_t* o_row, float* lse_at, int row, int keys,
-                                         int lane, bool write)
+__device__ __attribute__((noinline)) void rows_again(KernelArgs p, int start, int len, int head, int kv_head, int w0,
+                                                     float m, float l, bool redo, uint32_t lds)
 {
-    const int half = lane >> 5;
+    constexpr int TILE = 32 * D * 2;
+    // the same in every lane, which a call does not tell the compiler
+    start = __builtin_amdgcn_readfirstlane(start), len = __builtin_amdgcn_readfirstlane(len);
+    head = __builtin_amdgcn_readfirstlane(head), kv_head = __builtin_amdgcn_readfirstlane(kv_head);
+    w0 = __builtin_amdgcn_readfirstlane(w0), lds = __builtin_amdgcn_readfirstlane(lds);
+    const int lane = threadIdx.x & 63, half = lane >> 5, last = len - 1, row = min(w0 + (lane & 31), last);
+    const int64_t k_ld = p->k_ld, v_ld = p->v_ld, token = start + row;
+    const uint16_t* k_seq = p->k + start * k_ld + kv_head * p->k_hd;
+    const uint16_t* v_seq = p->v + start * v_ld + kv_head * p->v_hd;
+    if (!rows_non_finite<D, BN>(v_seq, v_ld, w0, last, lane)) return;
+
+    const uint16_t* q_row = p->q + token * p->q_ld + head * p->q_hd;
+    bf16x8 q[D / 16];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) q[ks] = *reinterpret_cast<const bf16x8*>(q_row + 16 * ks + 8 * half);
+    const float c = p->scale * LOG2E, mc = m * c;
+    const uint32_t rows_at = lds + rows_address<D>(lane), tr_at = lds + tr_address<D>(lane);
     f32x16 o[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll 1
-    for (int key = 0; key < keys; ++key) {
-        float dot = 0.0f;
-#pragma unroll 1
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const bf16x8 a = *reinterpret_cast<const bf16x8*>(q_row + 16 * ks + 8 * half);
-            const bf16x8 b = *reinterpret_cast<const bf16x8*>(k_seq + key * p.k_ld + 16 * ks + 8 * half);
+    for (int k0 = 0; k0 < w0; k0 += 32) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // the last tile has been read
+        stage<D, 32, 1>(uniform_ptr(k_seq + k0 * k_ld), (uint32_t)k_ld * 2, 31, lds, 0, lane);
+        stage<D, 32, 1>(uniform_ptr(v_seq + k0 * v_ld), (uint32_t)v_ld * 2, 31, lds + TILE, 0, lane);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        f32x16 s;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dot = __builtin_fmaf((float)a[j], (float)b[j], dot);
-        }
-        dot = (dot + swap_half(dot)) * p.scale * LOG2E;
-        if (key > row) continue;
-        // a NaN score makes the row NaN, as the definition does
-        const float top = dot > m || dot != dot ? dot : m;
-        const float base = top == -__builtin_inff() ? 0.0f : top;
-        const float old = __builtin_amdgcn_exp2f(m - base), pr = __builtin_amdgcn_exp2f(dot - base);
-        m = top;
-        l = l * old + pr;
+        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt)
+        for (int ks = 0; ks < D / 16; ++ks) s = mfma(read_rows_at(rows_at, ks, 0), q[ks], s);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const bf16x4 x = *reinterpret_cast<const bf16x4*>(v_seq + key * p.v_ld + 32 * dt + 8 * g + 4 * half);
+        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[dt][4 * g + j] = o[dt][4 * g + j] * old + pr * (float)x[j];
-            }
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+                o[dt] = mfma(read_tr_at<D>(tr_at, 16 * ks, dt, TILE), pack8(s, 8 * ks), o[dt]);
     }
-    store_row<D>(o_row, o, l == 0.0f ? 0.0f : 1.0f / l, lane, write);
-    if (write && half == 0) *lse_at = m * LN2 + __logf(l);
+#pragma unroll 1
+    for (int key = w0; key < min(w0 + 32, len); ++key) {
+        const float dot = dot_rows<D>(q_row, k_seq + key * k_ld, half);
+        if (key <= row) add_row<D>(o, __builtin_amdgcn_exp2f(__builtin_fmaf(dot, c, -mc)), v_seq + key * v_ld, half);
+    }
+    store_row<D>(p->o + token * p->o_ld + head * p->o_hd, o, l == 0.0f ? 0.0f : 1.0f / l, lane, redo);
 }
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
 {
     constexpr int TILE = BN * D * 2;
-    __shared__ __attribute__((aligned(16))) char lds[4 * TILE];   // K0 K1 V0 V1
+    __shared__ __attribute__((aligned(256))) char lds[4 * TILE];   // K0 K1 V0 V1
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -114,24 +131,25 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
     const int head = (group << p.hb_shift) + (wave & ((1 << p.hb_shift) - 1));
     const int w0 = t0 + (wave >> p.hb_shift) * 32;          // the wave's first token in the segment
     const int row = w0 + (lane & 31);
-    const bool write = row < at.len;
-    const int64_t token = at.start + (write ? row : at.len - 1);
-    uint16_t* o_row = p.o + token * p.o_ld + head * p.o_hd;
-    float* lse_at = p.lse + head * p.T + token;
+    auto token_of = [&](int row) { return at.start + min(row, at.len - 1); };
+    auto store = [&](const f32x16* o, float f, float lse) {
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));         // addresses formed here are not kept in registers until the end
+        const int row = w0 + (lane & 31);
+        const int64_t token = token_of(row);
+        store_row<D>(p.o + token * p.o_ld + head * p.o_hd, o, f, lane, row < at.len);
+        if (row < at.len && lane < 32) p.lse[head * p.T + token] = lse;
+    };
 
     f32x16 o[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] = 0.0f;
-    if (!at.sequence) {                                // tokens of no sequence see nothing
-        store_row<D>(o_row, o, 0.0f, lane, write);
-        if (write && half == 0) *lse_at = -__builtin_inff();
-        return;
-    }
+    if (!at.sequence) return store(o, 0.0f, -__builtin_inff());       // tokens of no sequence see nothing
 
     const int kv_head = (int)divide(group, p.share);
-    const uint16_t* q_row = p.q + token * p.q_ld + head * p.q_hd;
+    const uint16_t* q_row = p.q + token_of(row) * p.q_ld + head * p.q_hd;
     const uint16_t* k_seq = uniform_ptr(p.k + at.start * p.k_ld + kv_head * p.k_hd);
     const uint16_t* v_seq = uniform_ptr(p.v + at.start * p.v_ld + kv_head * p.v_hd);
     bf16x8 q[D / 16];
@@ -289,20 +307,15 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
         step(n, sa, sb);
         if (n + 1 < n_tiles) step(n + 1, sb, sa);
     }
+    publish();                                 // from here on each wave has a part of the tiles' place to itself
     if (w0 >= at.len) return;
     l += swap_half(l);
-    // 0 * x is NaN for a non-finite x and 0 otherwise
-    float bad = 0.0f * l;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) bad = __builtin_fmaf(0.0f, o[dt][i], bad);
-    bad += swap_half(bad);
-    const bool redo = bad != bad;
-    store_row<D>(o_row, o, l == 0.0f ? 0.0f : 1.0f / l, lane, write && !redo);
-    if (write && !redo && half == 0) *lse_at = m * p.scale + __logf(l);
-    if (__any(write && redo))
-        rows_by_key<D>(p, q_row, k_seq, v_seq, o_row, lse_at, row, wave_keys, lane, write && redo);
+    const bool redo = row < at.len && non_finite<D>(o);
+    store(o, l == 0.0f ? 0.0f : 1.0f / l, m * p.scale + __logf(l));
+    static_assert(2 * 32 * D * 2 <= TILE, "two tiles of 32 rows");
+    if (__any(redo))
+        rows_again<D>((KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(), (int)at.start, at.len, head, kv_head, w0, m, l,
+                      redo, base + wave * TILE);
 }
 
 } // namespace

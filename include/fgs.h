@@ -547,8 +547,12 @@ typedef struct {
  * head_dim 64 or 128; heads a multiple of kv_heads; scale finite and > 0.
  * Scores, softmax statistics and sums are FP32; the probabilities are rounded
  * to BF16 for the product with v.  A row depends on the tokens it sees alone:
- * NaN or Inf in later tokens or other sequences do not reach it.  A row whose
- * scores are all -Inf gets out = 0 and lse = -Inf.
+ * NaN or Inf in later tokens or other sequences do not reach it (rows that a
+ * tile of values with NaN or Inf may have reached are computed again, which
+ * takes a call to at most about 2.5 times its time).  A row whose scores are
+ * all -Inf gets lse = -Inf and 0 times the values it sees, 0 for finite ones.
+ * The sums over v precede their division by the row sum: |v| up to 2^80 cannot
+ * overflow them.
  */
 int fgs_attention_fwd(const fgs_heads *q, const fgs_heads *k, const fgs_heads *v,
                       const int32_t *cu_seqlens, int32_t num_seqs, int64_t tokens,
@@ -562,8 +566,10 @@ int fgs_attention_fwd(const fgs_heads *q, const fgs_heads *k, const fgs_heads *v
  *   fixed order: the same inputs give the same bits.  NaN or Inf reach what the
  *   formulas make depend on them and nothing else: in a token's q or dout, its
  *   dq and the dk, dv of the tokens that it sees; in its k or v, the dq of the
- *   tokens that see it, and what those rows reach.  (Rows that come out
- *   non-finite are computed again pair by pair, a slow path.)
+ *   tokens that see it, and what those rows reach.  (Rows and keys that hidden
+ *   pairs may have reached are computed again, which takes a call to at most
+ *   about 7 times its time: 8192 tokens, 32 heads of 128, NaN in the dout of
+ *   every token 10.1 ms, finite 1.9.)
  * Layouts, cu_seqlens and limits as fgs_attention_fwd.
  * workspace  DEVICE scratch, 16-byte aligned, of at least
  *   fgs_attention_workspace_bytes(tokens, heads) bytes.

@@ -1,0 +1,115 @@
+"""NaN and Inf in attention: which results they reach, at the places where the
+kernels' tiles mix hidden pairs with visible ones, and that a pass with them
+takes no longer than a small multiple of a finite one."""
+import time
+
+import pytest
+import torch
+
+import fine_grained_scaled_amd as fgs
+from _operator_refs import attention, pack_offsets, within
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+def _inputs(lengths, H, Hk, D, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    shapes = dict(q=H, k=Hk, v=Hk, dout=H)
+    return {n: torch.randn(sum(lengths), h, D, generator=g).to(torch.bfloat16) for n, h in shapes.items()}
+
+
+def _run(x, cu):
+    x = {n: t.cuda() for n, t in x.items()}
+    out, lse = fgs.attention_fwd(x["q"], x["k"], x["v"], cu)
+    grads = fgs.attention_bwd(x["dout"], x["q"], x["k"], x["v"], out, lse, cu)
+    return dict(zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)))
+
+
+# tokens of one sequence of 200: first and last of it and of blocks of 32 and
+# 64, several of one block, in the tail that a tile repeats
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens", [[0], [1], [31], [32], [63], [64, 65], [33, 40, 62], [96, 127], [191], [192, 199], [199],
+                                    [5, 70, 150]], ids=str)
+@pytest.mark.parametrize("where", ["q", "k", "v", "dout"])
+def test_only_what_depends_on_them(where, tokens, D):
+    lengths, H, Hk = [45, 200, 3], 6, 2
+    x = _inputs(lengths, H, Hk, D, seed=D + tokens[0])
+    cu = pack_offsets(lengths)
+    want = attention(x["q"], x["k"], x["v"], cu, D ** -0.5, x["dout"])
+    bad = {n: t.clone() for n, t in x.items()}
+    for i, t in enumerate(tokens):
+        bad[where][45 + t, :, (7 * t + 3) % D] = (NAN, INF, -INF)[i % 3]
+    got = _run(bad, cu.cuda())
+    every = torch.arange(sum(lengths))
+    other = (every < 45) | (every >= 245)
+    first, last = 45 + tokens[0], 45 + tokens[-1]
+    its_own = torch.zeros(248, dtype=torch.bool)
+    its_own[[45 + t for t in tokens]] = True
+    everything = torch.ones_like(its_own)
+    none_seen = other | (every < first)
+    keep = {"q": dict(out=~its_own, lse=~its_own, dq=~its_own, dk=other | (every > last), dv=other | (every > last)),
+            "dout": dict(out=everything, lse=everything, dq=~its_own, dk=other | (every > last), dv=other | (every > last)),
+            "k": dict(out=none_seen, lse=none_seen, dq=none_seen, dk=other, dv=other),
+            "v": dict(out=none_seen, lse=everything, dq=none_seen, dk=other, dv=other)}[where]
+    for name, rows in keep.items():
+        on, value = got[name].cpu(), want[name]
+        if name == "lse":
+            within(name, on[:, rows], [t[:, rows] for t in value])
+        else:
+            within(name, on[rows], [t[rows] for t in value])
+    if where == "v":       # and what does depend on them says so, in the columns that hold them
+        for t in tokens:
+            assert not got["out"][45 + t:245, :, (7 * t + 3) % D].isfinite().any()
+    if where == "dout":
+        for t in tokens:
+            assert not got["dv"][45:45 + t + 1, :, (7 * t + 3) % D].isfinite().any()
+            assert not got["dq"][45 + t].isfinite().any()
+
+
+def test_key_tiles_in_parts():
+    """A long sequence and one key head: the workgroup that adds the parts
+    forms the keys again over every part's queries."""
+    lengths, H, Hk, D = [30, 1300], 4, 1, 64
+    x = _inputs(lengths, H, Hk, D, seed=3)
+    cu = pack_offsets(lengths)
+    want = attention(x["q"], x["k"], x["v"], cu, D ** -0.5, x["dout"])
+    for t in (130, 517, 1000):                 # in the last heads alone
+        x["dout"][30 + t, 3, 9] = NAN
+    x["q"][30 + 700, 2, 1] = INF
+    got = _run(x, cu.cuda())
+    every = torch.arange(1330)
+    rows = (every < 30) | (every > 30 + 1000)
+    for name in ("dk", "dv"):
+        within(name, got[name].cpu()[rows], [t[rows] for t in want[name]])
+
+
+def _time(x, cu):
+    def once():
+        out, lse = fgs.attention_fwd(x["q"], x["k"], x["v"], cu)
+        fgs.attention_bwd(x["dout"], x["q"], x["k"], x["v"], out, lse, cu)
+        torch.cuda.synchronize()
+    once()
+    least = INF
+    for _ in range(3):
+        begin = time.perf_counter()
+        once()
+        least = min(least, time.perf_counter() - begin)
+    return least
+
+
+@pytest.mark.parametrize("what", ["last token", "every token", "one value a block"])
+@pytest.mark.parametrize("where", ["q", "k", "v", "dout"])
+def test_time(where, what):
+    """Every pair once more by tiles, with a load's latency a step, is below 20
+    passes; 64 keys or 32 queries a head pair by pair are below 2 ms.  (Every
+    pair one by one would be hundreds of passes.)"""
+    T, H, Hk, D = 4096, 8, 1, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = {n: torch.randn(T, h, D, generator=g, device="cuda").to(torch.bfloat16)
+         for n, h in dict(q=H, k=Hk, v=Hk, dout=H).items()}
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    finite = _time(x, cu)
+    at = {"last token": [T - 1], "every token": slice(None), "one value a block": slice(17, None, 32)}[what]
+    x[where][at, -1, 5] = NAN
+    assert _time(x, cu) <= 20 * finite + 2e-3
