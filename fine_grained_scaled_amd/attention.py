@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .ops import _stream_of
+from .ops import _readable, _stream_of
 
 _LIMIT = "must be a [tokens x heads x head_dim] bfloat16 tensor"
 _HEADS = 24      # bytes of an fgs_heads: pointer and two strides
@@ -102,13 +102,6 @@ def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     return dq, dk, dv
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """t itself where the kernels can read it, or else a copy laid out for them."""
-    if t.stride(2) == 1 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0:
-        return t
-    return t.contiguous()
-
-
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
@@ -121,7 +114,7 @@ class _Attention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, cu = ctx.saved_tensors
-        dq, dk, dv = attention_bwd(_rows(dout.to(torch.bfloat16)), q, k, v, out, lse, cu, ctx.scale)
+        dq, dk, dv = attention_bwd(_readable(dout.to(torch.bfloat16), 0), q, k, v, out, lse, cu, ctx.scale)
         return dq, dk, dv, None, None
 
 

@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from .ops import _need_gpu, _stream_of
+from .ops import _need_gpu, _readable, _stream_of
 
 _RESIDUAL = {torch.float32: _lib.OUT_FP32, torch.bfloat16: _lib.OUT_BF16}
 
@@ -127,8 +127,8 @@ class _ResidualNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dr, dn):
         y, r, w_pre, w_post, gate = ctx.saved_tensors
-        g = residual_norm_bwd(dr.contiguous(), dn.contiguous(), y, r, w_pre=w_pre, w_post=w_post, gate=gate,
-                              alpha=ctx.alpha, eps=ctx.eps)
+        dr, dn = _readable(dr, y.shape[1]), _readable(dn, y.shape[1])
+        g = residual_norm_bwd(dr, dn, y, r, w_pre=w_pre, w_post=w_post, gate=gate, alpha=ctx.alpha, eps=ctx.eps)
         return g.y, g.residual, g.w_pre, g.w_post, g.gate, None, None
 
 

@@ -40,6 +40,18 @@ def _stream_of(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _readable(t: torch.Tensor, least: int) -> torch.Tensor:
+    """t itself where the kernels can read it (unit stride along the last
+    dimension, other strides multiples of 8 and `least` at least, 16-byte
+    aligned), or else a copy laid out for them.  A gradient may arrive in any
+    layout, and contiguous() returns a contiguous one as it is, aligned or
+    not: torch.cat's are views at the places where their parts lay."""
+    *outer, unit = t.stride()
+    if unit == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 and s >= least for s in outer):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _need_gpu(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
