@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import fine_grained_scaled_amd as fgs
+from fine_grained_scaled_amd.attention import _strides
+from fine_grained_scaled_amd.norm import _matrix
 from fine_grained_scaled_amd.ops import _readable
 
 
@@ -63,3 +65,34 @@ def test_attention_after_cat():
         return [t.grad for t in on]
     for got, want in zip(grads(lambda t: _apart(t)[1:]), grads(torch.flatten)):
         assert torch.equal(got, want)
+
+
+def test_strides_of_single_rows_and_heads():
+    """The stride of a dimension of one entry means nothing: a transposed
+    column is a row with a stride of 1, and contiguous() leaves it so."""
+    row = torch.zeros(64, 1, dtype=torch.bfloat16).t()
+    assert row.stride() == (1, 1) and row.contiguous().stride() == (1, 1)
+    assert _matrix(row, "y", row.shape, torch.bfloat16, -1) == 64
+    odd = torch.zeros(5, 68, dtype=torch.bfloat16)[:, :64]
+    assert _matrix(odd[:1], "y", (1, 64), torch.bfloat16, -1) == 64
+    assert _matrix(odd, "y", odd.shape, torch.bfloat16, -1) == 68
+    assert _strides(torch.zeros(9, 68).as_strided((1, 4, 64), (3, 64, 1)), "q") == (256, 64)
+    assert _strides(torch.zeros(9, 64).as_strided((9, 1, 64), (64, 1, 1)), "k") == (64, 64)
+    assert _strides(torch.zeros(9, 4, 64), "q") == (256, 64)
+    assert _strides(torch.zeros(9, 1, 64).expand(-1, 4, -1), "k") == (64, 0)
+
+
+@pytest.mark.gpu
+def test_a_single_row_of_any_stride():
+    g = torch.Generator().manual_seed(2)
+    y, x = (torch.randn(64, 1, generator=g).to(torch.bfloat16).cuda().t() for _ in range(2))
+    assert y.stride(0) == 1
+    w = torch.ones(64, device="cuda")
+    for got, want in zip(fgs.residual_norm_fwd(y, x, w_pre=w),
+                         fgs.residual_norm_fwd(*(t.clone(memory_format=torch.contiguous_format) for t in (y, x)), w_pre=w)):
+        assert torch.equal(got, want)
+    q, k = torch.randn(1, 4, 64, generator=g).to(torch.bfloat16).cuda(), torch.randn(4, 1, 64, generator=g).to(torch.bfloat16).cuda()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    v = k[2:3]
+    odd = [t.as_strided(t.shape, (3, 64, 1)) for t in (q, v, v)]
+    assert torch.equal(fgs.attention_fwd(*odd, cu)[0], fgs.attention_fwd(q, v, v, cu)[0])
