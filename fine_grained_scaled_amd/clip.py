@@ -54,4 +54,5 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     _lib.check(lib.fgs_clip_grad_norm(
         table.buffer_info()[0], len(grads), max_norm, norm.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_of(norm)))
+    torch.autograd.graph.increment_version(out)      # written behind torch's back: graphs that saved them have to know
     return norm
