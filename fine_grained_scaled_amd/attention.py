@@ -66,7 +66,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     """Causal attention of every sequence of the pack: returns (out [T x H x D]
     bfloat16, lse [H x T] float32, the natural logarithm of the row sums).
     q is [T x H x D], k and v [T x Hk x D] (H a multiple of Hk, D 64 or 128),
-    views of a fused projection among them.  softmax_scale: 1 / sqrt(D).
+    views of a fused projection among them.  softmax_scale: 1 / sqrt(D)
+    unless given (2^-100 to 2^100).
     Tokens of no sequence get out = 0 and lse = -inf."""
     views = _heads(q, "q") + _heads(k, "k") + _heads(v, "v")
     T, H, Hk, D, scale = _check(q, k, v, cu_seqlens, softmax_scale)

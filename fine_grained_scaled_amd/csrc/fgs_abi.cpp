@@ -568,6 +568,8 @@ static int check_attention(const int32_t* cu, int32_t S, int64_t T, int32_t H, i
         return fail(FGS_ERR_INVALID_ARG, "heads (%d) must be a positive multiple of kv_heads (%d)", H, Hk);
     if (D != 64 && D != 128) return fail(FGS_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", D);
     if (!(scale > 0.0f) || scale > 3.4e38f) return fail(FGS_ERR_INVALID_ARG, "scale must be finite and > 0");
+    // beyond these the backward pass's -lse / scale, or scale * log2(e), may leave FP32
+    if (scale < 0x1p-100f || scale > 0x1p100f) return fail(FGS_ERR_UNSUPPORTED, "scale must be 2^-100 to 2^100 (got %g)", (double)scale);
     if (T == 0) return FGS_OK;
     if (!cu || !aligned(cu, 4)) return fail(FGS_ERR_INVALID_ARG, "cu_seqlens must be a 4-byte aligned device pointer");
     if (T > 0x7FFFFFFF - 256) return fail(FGS_ERR_UNSUPPORTED, "tokens too large (%lld)", (long long)T);

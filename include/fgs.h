@@ -544,7 +544,7 @@ typedef struct {
  *          decrease give unspecified values, but every access stays inside
  *          the tensors.
  * lse      FP32 [heads][tokens].
- * head_dim 64 or 128; heads a multiple of kv_heads; scale finite and > 0.
+ * head_dim 64 or 128; heads a multiple of kv_heads; scale 2^-100 to 2^100.
  * Scores, softmax statistics and sums are FP32; the probabilities are rounded
  * to BF16 for the product with v.  A row depends on the tokens it sees alone:
  * NaN or Inf in later tokens or other sequences do not reach it (rows that a
