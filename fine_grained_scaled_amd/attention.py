@@ -58,7 +58,7 @@ def _check(q, k, v, cu_seqlens, softmax_scale):
     gpu = q.get_device()
     if k.get_device() != gpu or v.get_device() != gpu or cu_seqlens.get_device() != gpu:
         raise ValueError("q, k, v and cu_seqlens must be on one GPU")
-    return T, H, Hk, D, (D ** -0.5 if softmax_scale is None else float(softmax_scale))
+    return T, H, Hk, D, (max(D, 1) ** -0.5 if softmax_scale is None else float(softmax_scale))
 
 
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,

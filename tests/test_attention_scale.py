@@ -4,8 +4,10 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from fine_grained_scaled_amd import _lib
+from fine_grained_scaled_amd.attention import _check
 
 FAKE = ctypes.c_void_p(0x10000)
 
@@ -41,3 +43,11 @@ def test_what_lies_beyond():
     every probability of the backward pass would be 0 instead of 1/2."""
     with np.errstate(over="ignore"):
         assert np.isinf(np.float32(np.log(2.0)) / np.float32(1e-39))
+
+
+def test_default():
+    """1 / sqrt(head_dim); heads of no value get as far as their refusal."""
+    cu = torch.zeros(2, dtype=torch.int32)
+    for dim, scale in ((64, 0.125), (0, 1.0)):
+        q = torch.zeros(3, 2, dim, dtype=torch.bfloat16)
+        assert _check(q, q, q, cu, None)[4] == scale
