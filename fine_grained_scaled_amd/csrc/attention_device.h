@@ -263,8 +263,9 @@ __device__ __forceinline__ void store_row(uint16_t* row, const f32x16* acc, floa
 // 1..S is sequence i - 1 and segment S + 1 what lies after cu[S]; segment i
 // owns the tiles from floor(start_i / rows) + i on, so a tile finds its
 // segment without a scan, and there are at most T / rows + S + 2 tiles.
-// Offsets that decrease or leave [0, T] are clamped: the rows touched stay
-// inside the buffers, whatever cu holds.
+// Offsets that leave [0, T] are clamped, and where they decrease a tile may
+// come out in front of its segment: it has no rows then.  The rows touched
+// stay inside the buffers, whatever cu holds.
 // ------------------------------------------------------------------------
 struct Where {
     int64_t start;   // first token of the segment
@@ -289,8 +290,9 @@ __device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, 
         const int seg = __popcll(__ballot(lane < S + 2 && (start >> shift) + lane <= tile)) - 1;
         const int a = __builtin_amdgcn_readlane(start, seg), b = __builtin_amdgcn_readlane(start, seg + 1);
         w.start = a;
-        w.tile = tile - ((a >> shift) + seg);
-        w.len = b > a && w.tile >= 0 ? b - a : 0;
+        const int at = tile - ((a >> shift) + seg);
+        w.tile = max(at, 0);
+        w.len = b > a && at >= 0 ? b - a : 0;
         w.sequence = seg > 0 && seg <= S;
         return w;
     }
@@ -302,8 +304,9 @@ __device__ __forceinline__ Where find_tile(const int32_t* cu, int S, int64_t T, 
     const int seg = __builtin_amdgcn_readfirstlane(n - 1);
     const int64_t a = segment_start(cu, S, T, seg), b = segment_start(cu, S, T, seg + 1);
     w.start = __builtin_amdgcn_readfirstlane((int)a);
-    w.tile = __builtin_amdgcn_readfirstlane(tile - ((int)(a >> shift) + seg));
-    w.len = __builtin_amdgcn_readfirstlane(b > a && w.tile >= 0 ? (int)(b - a) : 0);
+    const int at = __builtin_amdgcn_readfirstlane(tile - ((int)(a >> shift) + seg));
+    w.tile = max(at, 0);
+    w.len = __builtin_amdgcn_readfirstlane(b > a && at >= 0 ? (int)(b - a) : 0);
     w.sequence = seg > 0 && seg <= S;
     return w;
 }
