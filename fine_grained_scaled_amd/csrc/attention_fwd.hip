@@ -238,7 +238,8 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
                 if (32 * t + acc_row(i, 0) > seen) s[t][i] = -__builtin_inff();
     };
     auto exponents = [&](const f32x16 (&s)[2], uint32_t (&pr)[16]) {
-        const float mc = m * c;
+        float mc = m * c;
+        asm volatile("" : "+v"(mc));                   // nothing of this is formed before a branch to here
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 32; i += 2) exponent_pair(s, i, mc, sum, pr);
@@ -262,11 +263,14 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(FwdParams p)
         else sum = exponents(s, pr);
         // m only has to keep exp2 in range: it moves when a row's exponents
         // pass 2^14, or when nothing of the row is above 2^-60 yet, so most
-        // tiles never look for their maximum nor touch the output sums.
-        if (__any(!(sum <= 16384.0f) || (l == 0.0f && sum < 0x1p-60f))) {
+        // tiles never look for their maximum nor touch the output sums.  It
+        // moves for those rows alone, or a row's bits would depend on others'.
+        const bool moves = !(sum <= 16384.0f) || (l == 0.0f && sum < 0x1p-60f);
+        if (__any(moves)) {
             const float top = row_top(s);
-            const bool none = l + swap_half(l) == 0.0f;
-            const float to = none ? (top == -__builtin_inff() ? m : top) : fmaxf(m, top);
+            const float here = moves ? 1.0f : 0.0f, other = swap_half(here), l_other = swap_half(l);
+            const bool none = l + l_other == 0.0f, stays = here + other == 0.0f;
+            const float to = stays ? m : none ? (top == -__builtin_inff() ? m : top) : fmaxf(m, top);
             const float old = none ? 1.0f : __builtin_amdgcn_exp2f((m - to) * c);
             m = to;
             l *= old;

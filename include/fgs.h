@@ -547,7 +547,8 @@ typedef struct {
  * head_dim 64 or 128; heads a multiple of kv_heads; scale 2^-100 to 2^100.
  * Scores, softmax statistics and sums are FP32; the probabilities are rounded
  * to BF16 for the product with v.  A row depends on the tokens it sees alone:
- * NaN or Inf in later tokens or other sequences do not reach it (rows that a
+ * finite values in later tokens or other sequences change none of its bits,
+ * and NaN or Inf there do not reach it (rows that a
  * tile of values with NaN or Inf may have reached are computed again, which
  * takes a call to at most about 2.5 times its time).  A row whose scores are
  * all -Inf gets lse = -Inf and 0 times the values it sees, 0 for finite ones.
