@@ -6,9 +6,11 @@ A pack holds sequences of different lengths one after the other:
 cu_seqlens (int32 [S + 1] on the GPU) says where each begins and ends, and is
 read on the device, so no call waits for the GPU.  attention_fwd and
 attention_bwd keep no state and can be captured into a graph.  So can
-attention() and its backward pass, once no eager graph of the same leaves is
-alive: torch ties a leaf's gradient to the stream of the graph that holds it,
-and capturing a backward pass beside one ends the process.
+attention() and its backward pass, as any of torch's operations, once no eager
+graph of the same leaves is alive (its loss deleted): a leaf's AccumulateGrad
+node keeps the stream on which it was made for as long as a graph holds it, a
+captured backward pass would have to wait for that stream, which capture does
+not allow, and torch's backward thread ends the process with the error.
 """
 from __future__ import annotations
 

@@ -26,9 +26,9 @@
 // dq, and the same bits on every run.
 //
 // Measured: 8192 tokens, 32 heads of 128 over 8 key heads, dq 700 to 775 us and
-// dk, dv 1000 to 1120 us, 1.0 to 1.1 PFLOP/s of executed products, near the rate
+// dk, dv 1020 to 1120 us, 1.0 to 1.1 PFLOP/s of executed products, near the rate
 // of a large matrix product (1183 TFLOP/s); 7 documents in the same tokens,
-// 270 and 390 us; 9 documents in 4099 tokens, 16 heads of 64, 31 and 36 us.
+// 254 and 352 us; 9 documents in 4099 tokens, 16 heads of 64, 31 and 36 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -19,9 +19,9 @@
 // operand of O^T = V^T P^T (attention_device.h).
 //
 // Measured (a matrix product of 8192^3 reaches 1183 TFLOP/s): 16384 tokens, 16
-// heads of 128, 970 to 1010 us, 1.1 PFLOP/s, the matrix units 62% busy at the
+// heads of 128, 970 to 1030 us, 1.1 PFLOP/s, the matrix units 60% busy at the
 // clock that the power limit leaves; 61 prompts of 9 to 467 tokens, 32 heads,
-// 43 us, where 26 would move the bytes: half of a short workgroup's time is
+// 44 us, where 26 would move the bytes: half of a short workgroup's time is
 // what comes before and after its tiles.
 #include <type_traits>
 

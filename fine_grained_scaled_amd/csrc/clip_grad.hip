@@ -78,8 +78,9 @@ __device__ __forceinline__ void values(const uint4& v, float f[8])
     }
 }
 
-// the squares of elements e0 + tid * N .. of a chunk, e0 and e1 relative to
-// the tensor's aligned address, the tensor being elements [lo, hi) of it
+// the sum of the squares that this thread takes of a chunk, which is vectors
+// vec0 .. vec0 + vecs - 1 from the tensor's aligned address on, the tensor being
+// elements [lo, hi) from there
 template <bool BF16>
 __device__ __forceinline__ double chunk_squares(const char* base, int64_t vec0, uint32_t vecs, int64_t lo, int64_t hi)
 {

@@ -563,7 +563,11 @@ int fgs_attention_fwd(const fgs_heads *q, const fgs_heads *k, const fgs_heads *v
 /*
  * fgs_attention_bwd -- the gradients dq, dk, dv of fgs_attention_fwd from its
  *   inputs, its out and lse, and dout.  dk and dv sum over the query heads
- *   that share a key head.  Tokens of no sequence get zeros.  The sums have a
+ *   that share a key head.  Tokens of no sequence get zeros.  Probabilities and
+ *   score gradients are FP32, rounded to BF16 for the products with dout, q and k
+ *   (with their remainders for the first rows of a sequence: those below 64 in
+ *   dq, below 32 in dk and dv); sums are FP32.  delta = dout.out is of the
+ *   rounded out, past the first 64 rows.  The sums have a
  *   fixed order: the same inputs give the same bits.  NaN or Inf reach what the
  *   formulas make depend on them and nothing else: in a token's q or dout, its
  *   dq and the dk, dv of the tokens that it sees; in its k or v, the dq of the
@@ -641,7 +645,8 @@ size_t fgs_residual_norm_workspace_bytes(int64_t rows, int64_t width);
  * grads    HOST array of `count` entries, read during the call only: data and
  *          out (DEVICE, may be equal; any alignment of whole values), the
  *          number of values, and elem FGS_OUT_FP32 or FGS_OUT_BF16.  Tensors
- *          clipped in place are not written where c is 1.
+ *          clipped in place are not written where c is 1.  The entries must not
+ *          overlap otherwise, nor name a tensor twice.
  * norm     DEVICE FP32 [1].
  * Squares are summed in FP64, in a fixed order (no atomics).
  * workspace  DEVICE scratch, 16-byte aligned, of at least
