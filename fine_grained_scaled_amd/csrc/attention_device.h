@@ -4,7 +4,7 @@
 #pragma once
 
 #include "fgs_device.h"
-#include "fgs_internal.h"
+#include "operators_internal.h"
 
 namespace fgs {
 namespace attn {

@@ -20,7 +20,7 @@
 #include <cmath>
 
 #include "fgs_device.h"
-#include "fgs_internal.h"
+#include "operators_internal.h"
 
 namespace fgs {
 

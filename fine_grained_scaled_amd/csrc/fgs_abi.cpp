@@ -8,6 +8,7 @@
 #include <string>
 
 #include "fgs_internal.h"
+#include "operators_internal.h"
 
 namespace {
 

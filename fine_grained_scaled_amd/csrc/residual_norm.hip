@@ -30,7 +30,7 @@
 #include <algorithm>
 
 #include "fgs_device.h"
-#include "fgs_internal.h"
+#include "operators_internal.h"
 
 namespace fgs {
 
