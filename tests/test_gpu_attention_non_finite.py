@@ -113,3 +113,46 @@ def test_time(where, what):
     at = {"last token": [T - 1], "every token": slice(None), "one value a block": slice(17, None, 32)}[what]
     x[where][at, -1, 5] = NAN
     assert _time(x, cu) <= 20 * finite + 2e-3
+
+
+def _formula(x, cu, scale):
+    """The definition with every hidden pair left out of every sum."""
+    q, k, v, dout = (x[n].double() for n in ("q", "k", "v", "dout"))
+    H, G = q.shape[1], q.shape[1] // k.shape[1]
+    got = dict(out=torch.zeros_like(q), dq=torch.zeros_like(q), dk=torch.zeros_like(k), dv=torch.zeros_like(v))
+    for a, b in zip(cu[:-1].tolist(), cu[1:].tolist()):
+        seen = torch.ones(b - a, b - a, dtype=torch.bool).tril()
+        total = lambda terms, over: torch.where(seen[:, :, None], terms, 0.0).sum(over)
+        for h in range(H):
+            qh, kh, vh, g = q[a:b, None, h], k[None, a:b, h // G], v[None, a:b, h // G], dout[a:b, None, h]
+            z = torch.where(seen, (qh * kh).sum(2) * scale, -torch.inf)
+            p = torch.where(seen, torch.exp(z - torch.logsumexp(z, 1, keepdim=True)), 0.0)
+            got["out"][a:b, h] = out = total(p[:, :, None] * vh, 1)
+            ds = p * ((g * vh).sum(2) - (g[:, 0] * out).sum(1, keepdim=True))
+            got["dq"][a:b, h] = total(ds[:, :, None] * kh, 1) * scale
+            got["dk"][a:b, h // G] += total(ds[:, :, None] * qh, 0) * scale
+            got["dv"][a:b, h // G] += total(p[:, :, None] * g, 0)
+    return got
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_formula(seed):
+    """A few NaN and Inf anywhere: a result is finite where the definition's
+    is, and depends on none of them there, so it is what it is without them."""
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda of: of[int(torch.randint(len(of), (1,), generator=g))]
+    D, Hk = pick([64, 128]), pick([1, 2])
+    H = Hk * pick([1, 2, 3, 4])
+    lengths = [pick([1, 20, 33, 64, 100, 150]) for _ in range(pick([1, 2, 3]))]
+    x = _inputs(lengths, H, Hk, D, seed=seed)
+    cu = pack_offsets(lengths)
+    want = attention(x["q"], x["k"], x["v"], cu, D ** -0.5, x["dout"])
+    for _ in range(pick([1, 3, 9])):
+        where = pick(["q", "k", "v", "dout"])
+        at = tuple(int(torch.randint(n, (1,), generator=g)) for n in x[where].shape)
+        x[where][at] = NAN if where in ("q", "k") else pick([NAN, INF, -INF])
+    got = _run(x, cu.cuda())
+    for name, value in _formula(x, cu, D ** -0.5).items():
+        finite, on = value.isfinite(), got[name].cpu()
+        assert torch.equal(on.isfinite(), finite), name
+        within(name, on[finite], [t[finite] for t in want[name]])
