@@ -26,25 +26,16 @@ _LIMIT = "must be a [tokens x heads x head_dim] bfloat16 tensor"
 _HEADS = 24      # bytes of an fgs_heads: pointer and two strides
 
 
-def _strides(t: torch.Tensor, name: str):
-    """Token stride and head stride of t; of a single token or head, whose
-    stride means nothing and may be anything, one that the kernels take."""
-    tokens, heads, values = t.shape
-    token, head, value = t.stride()
-    if value != 1 and values > 1:
-        raise ValueError(f"{name} must have unit stride along head_dim")
-    if heads == 1:
-        head = values
-    return (token if tokens > 1 else heads * values), head
-
-
 def _heads(t: torch.Tensor, name: str):
     """The fgs_heads of t: pointer, token stride, head stride."""
     if t.dtype != torch.bfloat16 or t.dim() != 3:
         raise TypeError(f"{name} {_LIMIT}")
     if not t.is_cuda:
         raise ValueError("fine_grained_scaled_amd operates on GPU tensors only")
-    return (t.data_ptr(), *_strides(t, name))
+    token, head, value = t.stride()
+    if value != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride along head_dim")
+    return t.data_ptr(), token, head
 
 
 def _check(q, k, v, cu_seqlens, softmax_scale):

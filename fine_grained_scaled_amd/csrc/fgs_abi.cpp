@@ -548,16 +548,22 @@ int fgs_grouped_wgrad_block_scaled_fp8mma(const fgs_operand* A, const fgs_operan
     return wgrad_impl(A, B, group_offsets, G, total_T, M, N, C, ldc, out_dtype, stream, true);
 }
 
-static int check_heads(const fgs_heads* x, const char* name, int heads, int D, bool output)
+// The view that the kernels get: the stride of a single token or head, which
+// may be anything, is 0.
+static int check_heads(const fgs_heads* x, fgs_heads* to, const char* name, int64_t tokens, int heads, int D, bool output)
 {
     if (!x) return fail(FGS_ERR_INVALID_ARG, "%s is NULL", name);
     if (!x->data) return fail(FGS_ERR_INVALID_ARG, "%s.data is NULL", name);
+    *to = *x;
+    if (tokens == 1) to->ld_token = 0;
+    if (heads == 1) to->ld_head = 0;
+    x = to;
     if (x->ld_token < 0 || x->ld_head < 0) return fail(FGS_ERR_INVALID_ARG, "%s has a negative stride", name);
     if (!aligned(x->data, 16) || x->ld_token % 8 || x->ld_head % 8)
         return fail(FGS_ERR_UNSUPPORTED, "%s must be 16-byte aligned with strides that are multiples of 8", name);
     // a tile's rows are addressed by 24-bit products of row and byte stride
     if (x->ld_token >= (int64_t)1 << 23) return fail(FGS_ERR_UNSUPPORTED, "%s.ld_token must be below 2^23", name);
-    if (output && (x->ld_token < D || (heads > 1 && x->ld_head < D)))
+    if (output && ((tokens > 1 && x->ld_token < D) || (heads > 1 && x->ld_head < D)))
         return fail(FGS_ERR_INVALID_ARG, "%s is written and its rows must not overlap (strides below head_dim %d)", name, D);
     return FGS_OK;
 }
@@ -586,13 +592,13 @@ int fgs_attention_fwd(const fgs_heads* q, const fgs_heads* k, const fgs_heads* v
     int st = check_attention(cu_seqlens, num_seqs, tokens, heads, kv_heads, head_dim, scale);
     if (st != FGS_OK) return st;
     if (tokens == 0) return ok();
-    if ((st = check_heads(q, "q", heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(k, "k", kv_heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(v, "v", kv_heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(out, "out", heads, head_dim, true)) != FGS_OK) return st;
-    if (!lse || !aligned(lse, 4)) return fail(FGS_ERR_INVALID_ARG, "lse must be a 4-byte aligned device pointer");
     fgs::AttentionArgs a{};
-    a.q = *q, a.k = *k, a.v = *v, a.out = *out, a.lse = lse, a.cu_seqlens = cu_seqlens;
+    if ((st = check_heads(q, &a.q, "q", tokens, heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(k, &a.k, "k", tokens, kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(v, &a.v, "v", tokens, kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(out, &a.out, "out", tokens, heads, head_dim, true)) != FGS_OK) return st;
+    if (!lse || !aligned(lse, 4)) return fail(FGS_ERR_INVALID_ARG, "lse must be a 4-byte aligned device pointer");
+    a.lse = lse, a.cu_seqlens = cu_seqlens;
     a.T = tokens, a.S = num_seqs, a.H = heads, a.Hk = kv_heads, a.D = head_dim, a.scale = scale;
     return hip_status(fgs::launch_attention_fwd(a, static_cast<hipStream_t>(stream)), "attention_fwd launch");
 }
@@ -615,20 +621,19 @@ int fgs_attention_bwd(const fgs_heads* dout, const fgs_heads* q, const fgs_heads
     int st = check_attention(cu_seqlens, num_seqs, tokens, heads, kv_heads, head_dim, scale);
     if (st != FGS_OK) return st;
     if (tokens == 0) return ok();
-    if ((st = check_heads(dout, "dout", heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(q, "q", heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(k, "k", kv_heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(v, "v", kv_heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(out, "out", heads, head_dim, false)) != FGS_OK) return st;
-    if ((st = check_heads(dq, "dq", heads, head_dim, true)) != FGS_OK) return st;
-    if ((st = check_heads(dk, "dk", kv_heads, head_dim, true)) != FGS_OK) return st;
-    if ((st = check_heads(dv, "dv", kv_heads, head_dim, true)) != FGS_OK) return st;
+    fgs::AttentionArgs a{};
+    if ((st = check_heads(dout, &a.dout, "dout", tokens, heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(q, &a.q, "q", tokens, heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(k, &a.k, "k", tokens, kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(v, &a.v, "v", tokens, kv_heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(out, &a.out, "out", tokens, heads, head_dim, false)) != FGS_OK) return st;
+    if ((st = check_heads(dq, &a.dq, "dq", tokens, heads, head_dim, true)) != FGS_OK) return st;
+    if ((st = check_heads(dk, &a.dk, "dk", tokens, kv_heads, head_dim, true)) != FGS_OK) return st;
+    if ((st = check_heads(dv, &a.dv, "dv", tokens, kv_heads, head_dim, true)) != FGS_OK) return st;
     if (!lse || !aligned(lse, 4)) return fail(FGS_ERR_INVALID_ARG, "lse must be a 4-byte aligned device pointer");
     const size_t need = fgs_attention_workspace_bytes(tokens, heads);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
         return fail(FGS_ERR_INVALID_ARG, "attention_bwd needs a 16-byte aligned workspace of %zu bytes", need);
-    fgs::AttentionArgs a{};
-    a.q = *q, a.k = *k, a.v = *v, a.out = *out, a.dout = *dout, a.dq = *dq, a.dk = *dk, a.dv = *dv;
     a.lse = const_cast<float*>(lse), a.delta = static_cast<float*>(workspace), a.cu_seqlens = cu_seqlens;
     if (tokens >= fgs::ATTENTION_SPLIT_TOKENS) {
         char* at = static_cast<char*>(workspace) + ((size_t)tokens * heads * 8 + 15) / 16 * 16;
@@ -639,9 +644,11 @@ int fgs_attention_bwd(const fgs_heads* dout, const fgs_heads* q, const fgs_heads
     return hip_status(fgs::launch_attention_bwd(a, static_cast<hipStream_t>(stream)), "attention_bwd launch");
 }
 
-static int check_rows(const void* p, int64_t ld, int64_t width, const char* name)
+// (the stride of a single row may be anything)
+static int check_rows(const void* p, int64_t ld, int64_t rows, int64_t width, const char* name)
 {
     if (!p) return fail(FGS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (rows == 1) ld = width;
     if (ld < width) return fail(FGS_ERR_INVALID_ARG, "%s: row stride %lld < width %lld", name, (long long)ld, (long long)width);
     if (ld % 8 || !aligned(p, 16)) return fail(FGS_ERR_UNSUPPORTED, "%s must be 16-byte aligned with a row stride that is a multiple of 8", name);
     return FGS_OK;
@@ -661,7 +668,7 @@ static int check_norm(int residual_dtype, int64_t rows, int64_t width, const flo
     if (!w_pre || !aligned(w_pre, 16)) return fail(FGS_ERR_INVALID_ARG, "w_pre must be a 16-byte aligned device pointer");
     if (w_post && !aligned(w_post, 16)) return fail(FGS_ERR_UNSUPPORTED, "w_post must be 16-byte aligned");
     if (gate_kind == FGS_GATE_CHANNEL && (!gate || !aligned(gate, 16))) return fail(FGS_ERR_INVALID_ARG, "gate must be a 16-byte aligned device pointer");
-    if (gate_kind == FGS_GATE_TOKEN) return check_rows(gate, ldg, width, "gate");
+    if (gate_kind == FGS_GATE_TOKEN) return check_rows(gate, ldg, rows, width, "gate");
     return FGS_OK;
 }
 
@@ -673,10 +680,10 @@ int fgs_residual_norm_fwd(const void* y, int64_t ldy, const void* x, int64_t ldx
     int st = check_norm(residual_dtype, rows, width, w_post, gate, ldg, gate_kind, alpha, w_pre, eps);
     if (st != FGS_OK) return st;
     if (rows == 0) return ok();
-    if ((st = check_rows(y, ldy, width, "y")) != FGS_OK) return st;
-    if ((st = check_rows(x, ldx, width, "x")) != FGS_OK) return st;
-    if ((st = check_rows(r, width, width, "r")) != FGS_OK) return st;
-    if ((st = check_rows(n, width, width, "n")) != FGS_OK) return st;
+    if ((st = check_rows(y, ldy, rows, width, "y")) != FGS_OK) return st;
+    if ((st = check_rows(x, ldx, rows, width, "x")) != FGS_OK) return st;
+    if ((st = check_rows(r, width, rows, width, "r")) != FGS_OK) return st;
+    if ((st = check_rows(n, width, rows, width, "n")) != FGS_OK) return st;
     fgs::NormArgs a{};
     a.T = rows, a.W = width, a.y = y, a.x = x, a.gate = gate, a.ldy = ldy, a.ldx = ldx, a.ldg = ldg;
     a.fp32 = residual_dtype == FGS_OUT_FP32, a.gate_kind = gate_kind, a.w_post = w_post, a.w_pre = w_pre;
@@ -704,13 +711,13 @@ int fgs_residual_norm_bwd(const void* dr, int64_t lddr, const void* dn, int64_t 
     if (w_post && (!dw_post || !aligned(dw_post, 4))) return fail(FGS_ERR_INVALID_ARG, "dw_post must be a 4-byte aligned device pointer");
     if (gate_kind == FGS_GATE_CHANNEL && (!dgate || !aligned(dgate, 4))) return fail(FGS_ERR_INVALID_ARG, "dgate must be a 4-byte aligned device pointer");
     if (rows > 0) {
-        if ((st = check_rows(dr, lddr, width, "dr")) != FGS_OK) return st;
-        if ((st = check_rows(dn, lddn, width, "dn")) != FGS_OK) return st;
-        if ((st = check_rows(y, ldy, width, "y")) != FGS_OK) return st;
-        if ((st = check_rows(r, ldr, width, "r")) != FGS_OK) return st;
-        if ((st = check_rows(dx, width, width, "dx")) != FGS_OK) return st;
-        if ((st = check_rows(dy, width, width, "dy")) != FGS_OK) return st;
-        if (gate_kind == FGS_GATE_TOKEN && (st = check_rows(dgate, width, width, "dgate")) != FGS_OK) return st;
+        if ((st = check_rows(dr, lddr, rows, width, "dr")) != FGS_OK) return st;
+        if ((st = check_rows(dn, lddn, rows, width, "dn")) != FGS_OK) return st;
+        if ((st = check_rows(y, ldy, rows, width, "y")) != FGS_OK) return st;
+        if ((st = check_rows(r, ldr, rows, width, "r")) != FGS_OK) return st;
+        if ((st = check_rows(dx, width, rows, width, "dx")) != FGS_OK) return st;
+        if ((st = check_rows(dy, width, rows, width, "dy")) != FGS_OK) return st;
+        if (gate_kind == FGS_GATE_TOKEN && (st = check_rows(dgate, width, rows, width, "dgate")) != FGS_OK) return st;
     }
     const size_t need = fgs_residual_norm_workspace_bytes(rows, width);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)

@@ -29,8 +29,7 @@ def _at(t: Optional[torch.Tensor]) -> int:
 
 
 def _matrix(t: torch.Tensor, name: str, shape, dtype, gpu: int) -> int:
-    """t's row stride; of a single row, whose stride means nothing and may be
-    anything, its width."""
+    """t's row stride."""
     if t.dtype != dtype or t.shape != shape:
         raise TypeError(f"{name} must be a [{shape[0]} x {shape[1]}] {dtype} tensor (got {tuple(t.shape)} {t.dtype})")
     row, value = t.stride()
@@ -38,7 +37,7 @@ def _matrix(t: torch.Tensor, name: str, shape, dtype, gpu: int) -> int:
         raise ValueError(f"{name} must have unit stride along columns")
     if t.get_device() != gpu:
         raise ValueError("all tensors must be on one GPU")
-    return row if shape[0] > 1 else shape[1]
+    return row
 
 
 def _weight(t: torch.Tensor, name: str, width: int, gpu: int) -> None:

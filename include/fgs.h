@@ -536,7 +536,8 @@ typedef struct {
  *   z[u] = scale * q[t].k[u], out[t] = sum_u softmax(z)[u] v[u],
  *   lse[h][t] = log(sum_u exp(z[u])) (natural logarithm).
  * q, out   heads x head_dim per token; k, v: kv_heads x head_dim.  Pointers
- *          16-byte aligned, strides multiples of 8, ld_token < 2^23.
+ *          16-byte aligned, strides multiples of 8, ld_token < 2^23 (the
+ *          stride of a single token or head may be anything).
  * cu_seqlens  DEVICE int32 [num_seqs + 1], non-decreasing, in [0, tokens]:
  *          sequence s is tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (none
  *          is allowed).  Read on the device (no host synchronisation).
@@ -605,8 +606,8 @@ size_t fgs_attention_workspace_bytes(int64_t tokens, int32_t heads);
  *          [width]), FGS_GATE_TOKEN (BF16 [rows x width], row stride ldg).
  * w_post, w_pre  FP32 [width]; w_post may be NULL.
  * n        BF16 [rows x width], dense.
- * width and strides are multiples of 8, width <= 16384; pointers 16-byte
- * aligned; eps >= 0.  x and r, or y and n, may be the same tensor (dense).
+ * width and strides are multiples of 8 (a single row's stride may be
+ * anything), width <= 16384; pointers 16-byte aligned; eps >= 0.  x and r, or y and n, may be the same tensor (dense).
  * Statistics and sums are FP32; rows = 0 does nothing.
  */
 enum { FGS_GATE_NONE = 0, FGS_GATE_CHANNEL = 1, FGS_GATE_TOKEN = 2 };

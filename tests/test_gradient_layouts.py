@@ -1,11 +1,12 @@
 """Gradients reach a backward pass in whatever layout the rest of the graph
 gives them: each is read as it is or copied, and none is refused."""
+import ctypes
+
 import pytest
 import torch
 
 import fine_grained_scaled_amd as fgs
-from fine_grained_scaled_amd.attention import _strides
-from fine_grained_scaled_amd.norm import _matrix
+from fine_grained_scaled_amd import _lib
 from fine_grained_scaled_amd.ops import _readable
 
 
@@ -69,17 +70,27 @@ def test_attention_after_cat():
 
 def test_strides_of_single_rows_and_heads():
     """The stride of a dimension of one entry means nothing: a transposed
-    column is a row with a stride of 1, and contiguous() leaves it so."""
+    column is a row with a stride of 1, and contiguous() leaves it so.  Calls
+    that are not refused for a stride end at a NULL lse or n, before any HIP
+    call."""
     row = torch.zeros(64, 1, dtype=torch.bfloat16).t()
     assert row.stride() == (1, 1) and row.contiguous().stride() == (1, 1)
-    assert _matrix(row, "y", row.shape, torch.bfloat16, -1) == 64
-    odd = torch.zeros(5, 68, dtype=torch.bfloat16)[:, :64]
-    assert _matrix(odd[:1], "y", (1, 64), torch.bfloat16, -1) == 64
-    assert _matrix(odd, "y", odd.shape, torch.bfloat16, -1) == 68
-    assert _strides(torch.zeros(9, 68).as_strided((1, 4, 64), (3, 64, 1)), "q") == (256, 64)
-    assert _strides(torch.zeros(9, 64).as_strided((9, 1, 64), (64, 1, 1)), "k") == (64, 64)
-    assert _strides(torch.zeros(9, 4, 64), "q") == (256, 64)
-    assert _strides(torch.zeros(9, 1, 64).expand(-1, 4, -1), "k") == (64, 0)
+    lib, at, null = _lib.load(), ctypes.c_void_p(0x10000), ctypes.c_void_p(0)
+
+    def norm(rows, ld):
+        assert lib.fgs_residual_norm_fwd(at, ld, at, ld, 0, rows, 64, null, at, ld, 2, 1.0, at, 1e-6, at, null, null) < 0
+        return lib.fgs_last_error()
+    assert b"n is NULL" in norm(1, 1) and b"n is NULL" in norm(1, 68) and b"n is NULL" in norm(2, 64)
+    assert b"row stride" in norm(2, 1) and b"multiple of 8" in norm(2, 68)
+
+    def attention(tokens, heads, token, head):
+        view = lambda: (ctypes.c_int64 * 3)(0x10000, token, head)
+        assert lib.fgs_attention_fwd(view(), view(), view(), at, 1, tokens, heads, heads, 64, 0.125, view(), null, null) < 0
+        return lib.fgs_last_error()
+    for taken in ((1, 4, 3, 64), (9, 1, 64, 1), (1, 1, -1, 5), (9, 4, 256, 64)):
+        assert b"lse" in attention(*taken)
+    for refused in ((2, 4, 3, 64), (9, 2, 256, 1), (9, 1, -64, 5)):
+        assert b"stride" in attention(*refused)
 
 
 @pytest.mark.gpu
