@@ -13,6 +13,7 @@ SCALE_TENSOR, SCALE_TILE_1x128, SCALE_BLOCK_128x128, SCALE_MX32_E8M0, SCALE_NV16
 ROUND_RNE, ROUND_STOCHASTIC = 0, 1
 OUT_FP32, OUT_BF16 = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+INDEX_I32, INDEX_I64 = 0, 1
 TILE_AUTO, TILE_NARROW, TILE_WIDE = 0, 1, 2
 
 EXPORTS = (
@@ -44,6 +45,9 @@ EXPORTS = (
     "fgs_residual_norm_workspace_bytes",
     "fgs_clip_grad_norm",
     "fgs_clip_workspace_bytes",
+    "fgs_linear_cross_entropy_fwd",
+    "fgs_linear_cross_entropy_bwd",
+    "fgs_linear_cross_entropy_workspace_bytes",
     "fgs_last_error",
     "fgs_version",
 )
@@ -129,6 +133,10 @@ def load() -> ctypes.CDLL:
     lib.fgs_clip_grad_norm.argtypes = [P, I32, F32, P, P, SZ, P]
     lib.fgs_clip_workspace_bytes.argtypes = [I32]
     lib.fgs_clip_workspace_bytes.restype = SZ
+    lib.fgs_linear_cross_entropy_fwd.argtypes = [P, I64, P, I64, P, I32, I64, I64, I64, P, P, P, SZ, P]
+    lib.fgs_linear_cross_entropy_bwd.argtypes = [P, P, P, I64, P, I64, P, I32, P, I64, I64, I64, P, P, P, SZ, P]
+    lib.fgs_linear_cross_entropy_workspace_bytes.argtypes = [I64, I64, I64, I32]
+    lib.fgs_linear_cross_entropy_workspace_bytes.restype = SZ
     lib.fgs_last_error.restype = ctypes.c_char_p
     lib.fgs_version.restype = ctypes.c_char_p
     for name in ("fgs_quantize_blockwise", "fgs_quantize_blockwise_noalloc", "fgs_quantize_delayed", "fgs_quantize_mx", "fgs_quantize_nvfp4",
@@ -139,7 +147,8 @@ def load() -> ctypes.CDLL:
                  "fgs_quantize_grouped_colwise", "fgs_grouped_wgrad_block_scaled",
                  "fgs_swiglu_quantize_grouped", "fgs_gemm_block_scaled_fp8out",
                  "fgs_grouped_gemm_block_scaled_fp8out", "fgs_attention_fwd", "fgs_attention_bwd",
-                 "fgs_residual_norm_fwd", "fgs_residual_norm_bwd", "fgs_clip_grad_norm"):
+                 "fgs_residual_norm_fwd", "fgs_residual_norm_bwd", "fgs_clip_grad_norm",
+                 "fgs_linear_cross_entropy_fwd", "fgs_linear_cross_entropy_bwd"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

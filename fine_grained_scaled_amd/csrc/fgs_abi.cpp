@@ -731,6 +731,76 @@ int fgs_residual_norm_bwd(const void* dr, int64_t lddr, const void* dn, int64_t 
     return hip_status(fgs::launch_residual_norm_bwd(a, static_cast<hipStream_t>(stream)), "residual_norm_bwd launch");
 }
 
+static int check_head(int64_t T, int64_t V, int64_t K, int index_dtype)
+{
+    if (T < 0 || V < 1 || K < 1)
+        return fail(FGS_ERR_INVALID_ARG, "tokens (%lld) must be >= 0, vocab (%lld) and width (%lld) >= 1", (long long)T, (long long)V, (long long)K);
+    if (index_dtype != FGS_INDEX_I32 && index_dtype != FGS_INDEX_I64)
+        return fail(FGS_ERR_INVALID_ARG, "index_dtype %d is not FGS_INDEX_I32 or FGS_INDEX_I64", index_dtype);
+    if (K % 64 || K > 65536) return fail(FGS_ERR_UNSUPPORTED, "width must be a multiple of 64, at most 65536 (got %lld)", (long long)K);
+    if (T > (1 << 24) || V > (1 << 24) || ((T + 255) / 256) * ((V + 127) / 128) > 0x7FFFFFFF)
+        return fail(FGS_ERR_UNSUPPORTED, "tokens (%lld) or vocab (%lld) too large", (long long)T, (long long)V);
+    return FGS_OK;
+}
+
+size_t fgs_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int backward)
+{
+    if (check_head(tokens, vocab, width, FGS_INDEX_I32) != FGS_OK) return 0;
+    return fgs::cross_entropy_workspace_bytes(tokens, vocab, width, backward);
+}
+
+static int check_head_call(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* targets, int index_dtype,
+                           int64_t T, int64_t V, int64_t K, void* workspace, size_t workspace_bytes, int backward)
+{
+    int st = check_head(T, V, K, index_dtype);
+    if (st != FGS_OK) return st;
+    if ((st = check_rows(w, ldw, V, K, "w")) != FGS_OK) return st;
+    if (T > 0) {
+        if ((st = check_rows(x, ldx, T, K, "x")) != FGS_OK) return st;
+        if (!targets || !aligned(targets, index_dtype == FGS_INDEX_I64 ? 8 : 4))
+            return fail(FGS_ERR_INVALID_ARG, "targets must be an aligned device pointer");
+    }
+    const size_t need = fgs::cross_entropy_workspace_bytes(T, V, K, backward);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+        return fail(FGS_ERR_INVALID_ARG, "linear_cross_entropy needs a 16-byte aligned workspace of %zu bytes", need);
+    return FGS_OK;
+}
+
+int fgs_linear_cross_entropy_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* targets,
+                                 int index_dtype, int64_t tokens, int64_t vocab, int64_t width,
+                                 float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_head_call(x, ldx, w, ldw, targets, index_dtype, tokens, vocab, width, workspace, workspace_bytes, 0);
+    if (st != FGS_OK) return st;
+    if (tokens == 0) return ok();
+    if (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4))
+        return fail(FGS_ERR_INVALID_ARG, "loss and lse must be 4-byte aligned device pointers");
+    fgs::CrossEntropyArgs a{};
+    a.x = x, a.w = w, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = tokens, a.V = vocab, a.K = width;
+    a.wide = index_dtype == FGS_INDEX_I64, a.loss = loss, a.lse = lse, a.workspace = workspace;
+    return hip_status(fgs::launch_cross_entropy_fwd(a, static_cast<hipStream_t>(stream)), "linear_cross_entropy_fwd launch");
+}
+
+int fgs_linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* x, int64_t ldx,
+                                 const void* w, int64_t ldw, const void* targets, int index_dtype, const float* lse,
+                                 int64_t tokens, int64_t vocab, int64_t width, void* dx, void* dw,
+                                 void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_head_call(x, ldx, w, ldw, targets, index_dtype, tokens, vocab, width, workspace, workspace_bytes, 1);
+    if (st != FGS_OK) return st;
+    if ((st = check_rows(dw, width, vocab, width, "dw")) != FGS_OK) return st;
+    if (tokens > 0) {
+        if ((st = check_rows(dx, width, tokens, width, "dx")) != FGS_OK) return st;
+        if (!dloss || !lse || !aligned(dloss, 4) || !aligned(lse, 4) || !aligned(dlse, 4))
+            return fail(FGS_ERR_INVALID_ARG, "dloss, lse (and dlse, if given) must be 4-byte aligned device pointers");
+    }
+    fgs::CrossEntropyArgs a{};
+    a.x = x, a.w = w, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = tokens, a.V = vocab, a.K = width;
+    a.wide = index_dtype == FGS_INDEX_I64, a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dlse = dlse;
+    a.dx = dx, a.dw = dw, a.workspace = workspace;
+    return hip_status(fgs::launch_cross_entropy_bwd(a, static_cast<hipStream_t>(stream)), "linear_cross_entropy_bwd launch");
+}
+
 size_t fgs_clip_workspace_bytes(int32_t count) { return count < 0 ? 0 : fgs::clip_workspace_bytes(count); }
 
 int fgs_clip_grad_norm(const fgs_grad* grads, int32_t count, float max_norm, float* norm,

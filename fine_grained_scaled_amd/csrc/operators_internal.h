@@ -50,4 +50,18 @@ hipError_t launch_clip_grad_norm(const fgs_grad* grads, int32_t count, float max
                                  hipStream_t stream);
 size_t clip_workspace_bytes(int32_t count);
 
+// The output head with softmax cross entropy (cross_entropy.hip).
+struct CrossEntropyArgs {
+    const void *x, *w, *targets;    // BF16 [T][ldx], BF16 [V][ldw], int32 or (wide) int64 [T]
+    int64_t ldx, ldw, T, V, K;
+    int wide;
+    float *loss, *lse;              // [T]; the backward call reads lse
+    const float *dloss, *dlse;      // [T]; dlse may be nullptr
+    void *dx, *dw;                  // BF16 [T][K], [V][K]
+    void* workspace;
+};
+hipError_t launch_cross_entropy_fwd(const CrossEntropyArgs& a, hipStream_t stream);
+hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& a, hipStream_t stream);
+size_t cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t K, int backward);
+
 } // namespace fgs

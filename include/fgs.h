@@ -663,6 +663,53 @@ int fgs_clip_grad_norm(const fgs_grad *grads, int32_t count, float max_norm, flo
                        void *workspace, size_t workspace_bytes, void *stream);
 size_t fgs_clip_workspace_bytes(int32_t count);
 
+/* Token ids and targets. */
+enum { FGS_INDEX_I32 = 0, FGS_INDEX_I64 = 1 };
+
+/*
+ * fgs_linear_cross_entropy_fwd -- the output head with softmax cross entropy,
+ *   the logits never written ([DSV3] "Mixed precision framework" keeps the
+ *   output head out of FP8).  For every token with a target in [0, vocab):
+ *     z = x w^T,  lse = log sum_v exp z[v],  loss = lse - z[target].
+ *   A token whose target lies outside (-100, say) takes no part: loss 0, lse 0,
+ *   no gradient, and its row of x does not reach the others' results.
+ * x        BF16 [tokens x width], row stride ldx; w: BF16 [vocab x width], row
+ *          stride ldw.  width a multiple of 64, at most 65536; strides multiples of 8
+ *          (a single row's may be anything); pointers 16-byte aligned.
+ * targets  DEVICE int32 or int64 (index_dtype FGS_INDEX_*) [tokens].
+ * loss, lse  FP32 [tokens].
+ * Products are exact and summed in FP32, as are exponents.  A row whose
+ * logits hold NaN or +Inf has loss and lse NaN.
+ * workspace  DEVICE scratch, 16-byte aligned, of at least
+ *   fgs_linear_cross_entropy_workspace_bytes(tokens, vocab, width, 0) bytes.
+ */
+int fgs_linear_cross_entropy_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *targets,
+                                 int index_dtype, int64_t tokens, int64_t vocab, int64_t width,
+                                 float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * fgs_linear_cross_entropy_bwd -- the gradients of fgs_linear_cross_entropy_fwd from
+ *   its inputs, its lse, and the gradients dloss and dlse (NULL: none) of its
+ *   two results:
+ *     dz[v] = (dloss + dlse) exp(z[v] - lse) - dloss [v == target],
+ *     dx = dz w,  dw = dz^T x.
+ * dx       BF16 [tokens x width], dense, zeros for tokens without a target;
+ * dw       BF16 [vocab x width], dense.
+ * The logits are formed again, a piece of the vocabulary at a time.  dz is
+ * rounded to BF16 for the two products, after division by the largest |dloss|
+ * or |dlse| of the tokens with a target; sums are FP32, in a fixed order.
+ * workspace  DEVICE scratch, 16-byte aligned, of at least
+ *   fgs_linear_cross_entropy_workspace_bytes(tokens, vocab, width, 1) bytes.
+ */
+int fgs_linear_cross_entropy_bwd(const float *dloss, const float *dlse, const void *x, int64_t ldx,
+                                 const void *w, int64_t ldw, const void *targets, int index_dtype, const float *lse,
+                                 int64_t tokens, int64_t vocab, int64_t width, void *dx, void *dw,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace of the two calls above (backward 0 or 1); 0 for sizes that
+ * they refuse. */
+size_t fgs_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int backward);
+
 /* Device workspace needed by TENSOR-mode and NVFP4 quantization (bytes). */
 size_t fgs_workspace_bytes(int64_t rows, int64_t cols);
 
