@@ -6,18 +6,21 @@ from ._lib import (ELEM_E2M1, ELEM_E4M3, ELEM_E5M2, SCALE_BLOCK_128x128, SCALE_M
 from .attention import attention, attention_bwd, attention_fwd
 from .clip import clip_grad_norm
 from .cross_entropy import linear_cross_entropy, linear_cross_entropy_bwd, linear_cross_entropy_fwd
+from .embedding import embedding, embedding_bwd, embedding_fwd
 from .linear import DelayedState, Linear, fp8_linear
 from .norm import ResidualNormGrads, residual_norm, residual_norm_bwd, residual_norm_fwd
 from .ops import (Operand, Quantized, gemm_block_scaled, gemm_block_scaled_fp8out, gemm_kernel_name,
                   grouped_colwise_blocks, grouped_gemm_block_scaled, grouped_gemm_block_scaled_fp8out, grouped_wgrad_block_scaled, quantize_blockwise,
                   quantize_delayed, quantize_grouped_colwise, quantize_mx, quantize_nvfp4,
                   swiglu_quantize_grouped)
+from .swiglu import swiglu, swiglu_bwd, swiglu_fwd
 
 __all__ = [
     "Linear", "fp8_linear", "DelayedState",
     "attention", "attention_fwd", "attention_bwd",
     "residual_norm", "residual_norm_fwd", "residual_norm_bwd", "ResidualNormGrads", "clip_grad_norm",
     "linear_cross_entropy", "linear_cross_entropy_fwd", "linear_cross_entropy_bwd",
+    "embedding", "embedding_fwd", "embedding_bwd", "swiglu", "swiglu_fwd", "swiglu_bwd",
     "gemm_block_scaled_fp8out", "grouped_gemm_block_scaled_fp8out", "gemm_kernel_name",
     "quantize_blockwise", "quantize_delayed", "quantize_mx", "quantize_nvfp4", "gemm_block_scaled",
     "grouped_gemm_block_scaled", "quantize_grouped_colwise", "grouped_colwise_blocks",

@@ -48,6 +48,11 @@ EXPORTS = (
     "fgs_linear_cross_entropy_fwd",
     "fgs_linear_cross_entropy_bwd",
     "fgs_linear_cross_entropy_workspace_bytes",
+    "fgs_embedding_fwd",
+    "fgs_embedding_bwd",
+    "fgs_embedding_workspace_bytes",
+    "fgs_swiglu_fwd",
+    "fgs_swiglu_bwd",
     "fgs_last_error",
     "fgs_version",
 )
@@ -137,6 +142,12 @@ def load() -> ctypes.CDLL:
     lib.fgs_linear_cross_entropy_bwd.argtypes = [P, P, P, I64, P, I64, P, I32, P, I64, I64, I64, P, P, P, SZ, P]
     lib.fgs_linear_cross_entropy_workspace_bytes.argtypes = [I64, I64, I64, I32]
     lib.fgs_linear_cross_entropy_workspace_bytes.restype = SZ
+    lib.fgs_embedding_fwd.argtypes = [P, I32, I64, P, I64, I32, I64, I64, F32, P, I32, P]
+    lib.fgs_embedding_bwd.argtypes = [P, I64, I32, P, I32, I64, I64, I64, F32, P, I32, I32, P, SZ, P]
+    lib.fgs_embedding_workspace_bytes.argtypes = [I64, I64]
+    lib.fgs_embedding_workspace_bytes.restype = SZ
+    lib.fgs_swiglu_fwd.argtypes = [P, I64, I64, I64, P, P, P, P]
+    lib.fgs_swiglu_bwd.argtypes = [P, I64, P, I64, P, P, I64, I64, P, P]
     lib.fgs_last_error.restype = ctypes.c_char_p
     lib.fgs_version.restype = ctypes.c_char_p
     for name in ("fgs_quantize_blockwise", "fgs_quantize_blockwise_noalloc", "fgs_quantize_delayed", "fgs_quantize_mx", "fgs_quantize_nvfp4",
@@ -148,7 +159,8 @@ def load() -> ctypes.CDLL:
                  "fgs_swiglu_quantize_grouped", "fgs_gemm_block_scaled_fp8out",
                  "fgs_grouped_gemm_block_scaled_fp8out", "fgs_attention_fwd", "fgs_attention_bwd",
                  "fgs_residual_norm_fwd", "fgs_residual_norm_bwd", "fgs_clip_grad_norm",
-                 "fgs_linear_cross_entropy_fwd", "fgs_linear_cross_entropy_bwd"):
+                 "fgs_linear_cross_entropy_fwd", "fgs_linear_cross_entropy_bwd",
+                 "fgs_embedding_fwd", "fgs_embedding_bwd", "fgs_swiglu_fwd", "fgs_swiglu_bwd"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

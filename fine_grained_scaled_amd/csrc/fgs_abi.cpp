@@ -738,7 +738,8 @@ static int check_head(int64_t T, int64_t V, int64_t K, int index_dtype)
     if (index_dtype != FGS_INDEX_I32 && index_dtype != FGS_INDEX_I64)
         return fail(FGS_ERR_INVALID_ARG, "index_dtype %d is not FGS_INDEX_I32 or FGS_INDEX_I64", index_dtype);
     if (K % 64 || K > 65536) return fail(FGS_ERR_UNSUPPORTED, "width must be a multiple of 64, at most 65536 (got %lld)", (long long)K);
-    if (T > (1 << 24) || V > (1 << 24) || ((T + 255) / 256) * ((V + 127) / 128) > 0x7FFFFFFF)
+    // a launch has fewer than 2^32 threads
+    if (T > (1 << 23) || V > (1 << 24) || ((T + 255) / 256) * ((V + 127) / 128) > (1 << 22))
         return fail(FGS_ERR_UNSUPPORTED, "tokens (%lld) or vocab (%lld) too large", (long long)T, (long long)V);
     return FGS_OK;
 }
@@ -799,6 +800,115 @@ int fgs_linear_cross_entropy_bwd(const float* dloss, const float* dlse, const vo
     a.wide = index_dtype == FGS_INDEX_I64, a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dlse = dlse;
     a.dx = dx, a.dw = dw, a.workspace = workspace;
     return hip_status(fgs::launch_cross_entropy_bwd(a, static_cast<hipStream_t>(stream)), "linear_cross_entropy_bwd launch");
+}
+
+static int check_embedding(const void* tokens, int index_dtype, int64_t count, int64_t V, int64_t W, float scale,
+                           int weight_dtype, int dtype)
+{
+    if (count < 0 || V < 1 || W < 1)
+        return fail(FGS_ERR_INVALID_ARG, "count (%lld) must be >= 0, vocab (%lld) and width (%lld) >= 1", (long long)count, (long long)V, (long long)W);
+    if (index_dtype != FGS_INDEX_I32 && index_dtype != FGS_INDEX_I64)
+        return fail(FGS_ERR_INVALID_ARG, "index_dtype %d is not FGS_INDEX_I32 or FGS_INDEX_I64", index_dtype);
+    for (int d : {weight_dtype, dtype})
+        if (d != FGS_OUT_FP32 && d != FGS_OUT_BF16) return fail(FGS_ERR_INVALID_ARG, "dtype %d is not FGS_OUT_FP32 or FGS_OUT_BF16", d);
+    if (!(scale - scale == 0.0f)) return fail(FGS_ERR_INVALID_ARG, "scale must be finite");
+    if (W % 8 || W > 65536) return fail(FGS_ERR_UNSUPPORTED, "width must be a multiple of 8, at most 65536 (got %lld)", (long long)W);
+    if (V > 0x7FFFFFFE) return fail(FGS_ERR_UNSUPPORTED, "vocab too large (%lld)", (long long)V);
+    if (count > 0 && (!tokens || !aligned(tokens, index_dtype == FGS_INDEX_I64 ? 8 : 4)))
+        return fail(FGS_ERR_INVALID_ARG, "tokens must be an aligned device pointer");
+    return FGS_OK;
+}
+
+int fgs_embedding_fwd(const void* tokens, int index_dtype, int64_t count, const void* weight, int64_t ldw,
+                      int weight_dtype, int64_t vocab, int64_t width, float scale, void* out, int out_dtype, void* stream)
+{
+    int st = check_embedding(tokens, index_dtype, count, vocab, width, scale, weight_dtype, out_dtype);
+    if (st != FGS_OK) return st;
+    if (count >= 1 << 24) return fail(FGS_ERR_UNSUPPORTED, "count too large (%lld)", (long long)count);
+    if (count == 0) return ok();
+    if ((st = check_rows(weight, ldw, vocab, width, "weight")) != FGS_OK) return st;
+    if ((st = check_rows(out, width, count, width, "out")) != FGS_OK) return st;
+    fgs::EmbeddingArgs a{};
+    a.tokens = tokens, a.wide = index_dtype == FGS_INDEX_I64, a.T = count, a.V = vocab, a.W = width;
+    a.weight = weight, a.ldw = ldw, a.weight_bf16 = weight_dtype == FGS_OUT_BF16, a.bf16 = out_dtype == FGS_OUT_BF16;
+    a.scale = scale, a.out = out;
+    return hip_status(fgs::launch_embedding_fwd(a, static_cast<hipStream_t>(stream)), "embedding_fwd launch");
+}
+
+constexpr int64_t kMaxGradientTokens = (int64_t)1 << 22;      // beyond, the sort's searches would cost more than the sums
+
+size_t fgs_embedding_workspace_bytes(int64_t count, int64_t width)
+{
+    if (count < 0 || count > kMaxGradientTokens || width < 1 || width % 8 || width > 65536) return 0;
+    return fgs::embedding_workspace_bytes(count, width);
+}
+
+int fgs_embedding_bwd(const void* dout, int64_t ldd, int dout_dtype, const void* tokens, int index_dtype, int64_t count,
+                      int64_t vocab, int64_t width, float scale, void* dweight, int dweight_dtype, int accumulate,
+                      void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_embedding(tokens, index_dtype, count, vocab, width, scale, dweight_dtype, dout_dtype);
+    if (st != FGS_OK) return st;
+    if (count > kMaxGradientTokens) return fail(FGS_ERR_UNSUPPORTED, "count too large (%lld)", (long long)count);
+    if ((st = check_rows(dweight, width, vocab, width, "dweight")) != FGS_OK) return st;
+    if (count > 0) {
+        if ((st = check_rows(dout, ldd, count, width, "dout")) != FGS_OK) return st;
+        const size_t need = fgs::embedding_workspace_bytes(count, width);
+        if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+            return fail(FGS_ERR_INVALID_ARG, "embedding_bwd needs a 16-byte aligned workspace of %zu bytes", need);
+    }
+    fgs::EmbeddingArgs a{};
+    a.tokens = tokens, a.wide = index_dtype == FGS_INDEX_I64, a.T = count, a.V = vocab, a.W = width;
+    a.weight_bf16 = dweight_dtype == FGS_OUT_BF16, a.bf16 = dout_dtype == FGS_OUT_BF16, a.scale = scale;
+    a.dout = dout, a.ldd = ldd, a.dweight = dweight, a.add = accumulate != 0, a.workspace = workspace;
+    return hip_status(fgs::launch_embedding_bwd(a, static_cast<hipStream_t>(stream)), "embedding_bwd launch");
+}
+
+static int check_swiglu(int64_t rows, int64_t inter)
+{
+    if (rows < 0 || inter < 0) return fail(FGS_ERR_INVALID_ARG, "rows (%lld) and inter (%lld) must be >= 0", (long long)rows, (long long)inter);
+    if (inter % 8 || inter > (int64_t)1 << 30) return fail(FGS_ERR_UNSUPPORTED, "inter must be a multiple of 8, at most 2^30 (got %lld)", (long long)inter);
+    if ((rows + 15) / 16 > kMaxRowBlocks) return fail(FGS_ERR_UNSUPPORTED, "rows too large (%lld)", (long long)rows);
+    return FGS_OK;
+}
+
+static int check_kept(const uint8_t* q, const float* scales)
+{
+    if (!q) return FGS_OK;
+    if (!scales || !aligned(scales, 4)) return fail(FGS_ERR_INVALID_ARG, "scales must be a 4-byte aligned device pointer");
+    if (!aligned(q, 16)) return fail(FGS_ERR_UNSUPPORTED, "q must be 16-byte aligned");
+    return FGS_OK;
+}
+
+int fgs_swiglu_fwd(const void* gate_up, int64_t rows, int64_t inter, int64_t ld, void* h, uint8_t* q, float* scales,
+                   void* stream)
+{
+    int st = check_swiglu(rows, inter);
+    if (st != FGS_OK) return st;
+    if (rows == 0 || inter == 0) return ok();
+    if ((st = check_rows(gate_up, ld, rows, 2 * inter, "gate_up")) != FGS_OK) return st;
+    if ((st = check_rows(h, inter, rows, inter, "h")) != FGS_OK) return st;
+    if ((st = check_kept(q, scales)) != FGS_OK) return st;
+    fgs::SwigluArgs a{};
+    a.T = rows, a.I = inter, a.gate_up = gate_up, a.ld = ld, a.h = h, a.q = q, a.scales = scales;
+    return hip_status(fgs::launch_swiglu_fwd(a, static_cast<hipStream_t>(stream)), "swiglu_fwd launch");
+}
+
+int fgs_swiglu_bwd(const void* dh, int64_t lddh, const void* gate_up, int64_t ld, const uint8_t* q, const float* scales,
+                   int64_t rows, int64_t inter, void* dgate_up, void* stream)
+{
+    int st = check_swiglu(rows, inter);
+    if (st != FGS_OK) return st;
+    if (rows == 0 || inter == 0) return ok();
+    if ((gate_up != nullptr) == (q != nullptr)) return fail(FGS_ERR_INVALID_ARG, "one of gate_up and q must be given, the other NULL");
+    if (gate_up && (st = check_rows(gate_up, ld, rows, 2 * inter, "gate_up")) != FGS_OK) return st;
+    if ((st = check_rows(dh, lddh, rows, inter, "dh")) != FGS_OK) return st;
+    if ((st = check_rows(dgate_up, 2 * inter, rows, 2 * inter, "dgate_up")) != FGS_OK) return st;
+    if ((st = check_kept(q, scales)) != FGS_OK) return st;
+    fgs::SwigluArgs a{};
+    a.T = rows, a.I = inter, a.gate_up = gate_up, a.ld = ld, a.q = const_cast<uint8_t*>(q), a.scales = const_cast<float*>(scales);
+    a.dh = dh, a.ldh = lddh, a.dgate_up = dgate_up;
+    return hip_status(fgs::launch_swiglu_bwd(a, static_cast<hipStream_t>(stream)), "swiglu_bwd launch");
 }
 
 size_t fgs_clip_workspace_bytes(int32_t count) { return count < 0 ? 0 : fgs::clip_workspace_bytes(count); }

@@ -64,4 +64,39 @@ hipError_t launch_cross_entropy_fwd(const CrossEntropyArgs& a, hipStream_t strea
 hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& a, hipStream_t stream);
 size_t cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t K, int backward);
 
+// Token embedding and its gradient (embedding.hip).
+struct EmbeddingArgs {
+    const void* tokens;             // int32 or (wide) int64 [T]
+    int wide;
+    int64_t T, V, W;
+    const void* weight;             // forward: [V][ldw]
+    int64_t ldw;
+    int weight_bf16, bf16;          // the weight's (gradient's) type, and that of out (dout): BF16, not FP32
+    float scale;
+    void* out;                      // [T][W]
+    const void* dout;               // backward: [T][ldd]
+    int64_t ldd;
+    void* dweight;                  // [V][W]
+    int add;                        // to what dweight holds
+    void* workspace;
+};
+hipError_t launch_embedding_fwd(const EmbeddingArgs& a, hipStream_t stream);
+hipError_t launch_embedding_bwd(const EmbeddingArgs& a, hipStream_t stream);
+size_t embedding_workspace_bytes(int64_t T, int64_t W);
+
+// SwiGLU with its input kept in 8 bits (swiglu.hip).
+struct SwigluArgs {
+    int64_t T, I;
+    const void* gate_up;            // BF16 [T][ld]
+    int64_t ld;
+    void* h;                        // BF16 [T][I]
+    uint8_t* q;                     // E4M3 [T][2 I], or nullptr: nothing kept (the backward call reads gate_up)
+    float* scales;                  // [2 ceil(I / 128)][T]
+    const void* dh;                 // BF16 [T][ldh]
+    int64_t ldh;
+    void* dgate_up;                 // BF16 [T][2 I]
+};
+hipError_t launch_swiglu_fwd(const SwigluArgs& a, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t stream);
+
 } // namespace fgs

@@ -675,7 +675,8 @@ enum { FGS_INDEX_I32 = 0, FGS_INDEX_I64 = 1 };
  *   no gradient, and its row of x does not reach the others' results.
  * x        BF16 [tokens x width], row stride ldx; w: BF16 [vocab x width], row
  *          stride ldw.  width a multiple of 64, at most 65536; strides multiples of 8
- *          (a single row's may be anything); pointers 16-byte aligned.
+ *          (a single row's may be anything); pointers 16-byte aligned.  At most
+ *          2^23 tokens and 2^22 tiles of 256 tokens and 128 words.
  * targets  DEVICE int32 or int64 (index_dtype FGS_INDEX_*) [tokens].
  * loss, lse  FP32 [tokens].
  * Products are exact and summed in FP32, as are exponents.  A row whose
@@ -709,6 +710,68 @@ int fgs_linear_cross_entropy_bwd(const float *dloss, const float *dlse, const vo
 /* Device workspace of the two calls above (backward 0 or 1); 0 for sizes that
  * they refuse. */
 size_t fgs_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int backward);
+
+/*
+ * fgs_embedding_fwd -- token embedding: out[t] = scale * weight[tokens[t]], zeros
+ *   for a token outside [0, vocab) ([DSV3] "Mixed precision framework" keeps the
+ *   embedding out of FP8).
+ * tokens   DEVICE int32 or int64 (index_dtype FGS_INDEX_*) [count].
+ * weight   FP32 or BF16 (weight_dtype FGS_OUT_*) [vocab x width], row stride ldw.
+ * out      FP32 or BF16 (out_dtype) [count x width], dense; the product is FP32,
+ *          rounded once.
+ * width a multiple of 8, at most 65536; strides multiples of 8 (a single row's
+ * may be anything); pointers 16-byte aligned; scale finite; fewer than 2^24 tokens.
+ */
+int fgs_embedding_fwd(const void *tokens, int index_dtype, int64_t count, const void *weight, int64_t ldw,
+                      int weight_dtype, int64_t vocab, int64_t width, float scale, void *out, int out_dtype, void *stream);
+
+/*
+ * fgs_embedding_bwd -- the gradient of fgs_embedding_fwd for the weight:
+ *   dweight[v] = scale * sum of dout[t] over the t with tokens[t] = v.
+ * dout     FP32 or BF16 (dout_dtype) [count x width], row stride ldd.  Rows of
+ *          tokens outside [0, vocab) reach nothing.
+ * dweight  FP32 or BF16 (dweight_dtype) [vocab x width], dense.  accumulate 0: every
+ *          row is written, zeros for a v without tokens; 1: the sums are added to
+ *          what it holds, and rows without tokens are neither read nor
+ *          written (the gradient of a tied output head, or of earlier batches).
+ * Sums are FP32 in an order that the tokens alone fix (no atomics): the same
+ * inputs give the same bits.  At most 2^22 tokens a call.
+ * workspace  DEVICE scratch, 16-byte aligned, of at least
+ *   fgs_embedding_workspace_bytes(count, width) bytes.
+ */
+int fgs_embedding_bwd(const void *dout, int64_t ldd, int dout_dtype, const void *tokens, int index_dtype, int64_t count,
+                      int64_t vocab, int64_t width, float scale, void *dweight, int dweight_dtype, int accumulate,
+                      void *workspace, size_t workspace_bytes, void *stream);
+size_t fgs_embedding_workspace_bytes(int64_t count, int64_t width);
+
+/*
+ * fgs_swiglu_fwd -- the MLP's activation, and its input kept in 8 bits for the
+ *   backward pass: h = g sigmoid(g) u of gate_up = [g | u].
+ * gate_up  BF16 [rows x 2*inter], row stride ld: g = columns 0..inter-1, u the
+ *          others.  h: BF16 [rows x inter], dense, within one BF16 ulp of the exact
+ *          value (results below 2^-120 may be 0).
+ * q, scales  NULL, or the kept input: the 1x128 quantization of each half ([DSV3]
+ *          "Fine-grained quantization", "Online quantization"; inter need not be a
+ *          multiple of 128: a half's last tile is shorter then).  q E4M3
+ *          [rows x 2*inter], dense; scales FP32 [2 * ceil(inter / 128)][rows], g's
+ *          tiles first: where inter is a multiple of 128, what
+ *          fgs_quantize_blockwise gives for gate_up.
+ * inter and strides multiples of 8 (a single row's stride may be anything);
+ * pointers 16-byte aligned.
+ */
+int fgs_swiglu_fwd(const void *gate_up, int64_t rows, int64_t inter, int64_t ld, void *h, uint8_t *q, float *scales,
+                   void *stream);
+
+/*
+ * fgs_swiglu_bwd -- the gradient of fgs_swiglu_fwd for gate_up, from dh (BF16, row
+ *   stride lddh) and the kept input:
+ *     dg = dh u sigmoid(g) (1 + g (1 - sigmoid(g))),  du = dh g sigmoid(g)
+ *   at the values that q and scales stand for (gate_up NULL), or at gate_up
+ *   itself (q NULL).  dgate_up: BF16 [rows x 2*inter], dense.  A tile that held
+ *   NaN or Inf was kept as NaN: all of its gradients are NaN.
+ */
+int fgs_swiglu_bwd(const void *dh, int64_t lddh, const void *gate_up, int64_t ld, const uint8_t *q, const float *scales,
+                   int64_t rows, int64_t inter, void *dgate_up, void *stream);
 
 /* Device workspace needed by TENSOR-mode and NVFP4 quantization (bytes). */
 size_t fgs_workspace_bytes(int64_t rows, int64_t cols);
