@@ -18,6 +18,9 @@
 // mostly masked tokens costs what its targets cost, and NaN in the rows of the
 // others reach nothing.
 //
+// The pieces' width and the number of workgroups that share a tile of dx follow
+// from that list too, on the device: few rows take wide pieces.
+//
 // dz goes to the matrix units in BF16, divided by the largest |dloss| (|dlse|)
 // of the call, which the results are multiplied with again in FP32: under a
 // mean over the tokens the values are then softmax - onehot itself, whose
@@ -34,14 +37,14 @@ namespace {
 using namespace prod;
 
 using Big = Shape<2, 4, 4, 2>;         // 256 x 256, 8 waves of 128 x 64
-using Small = Shape<1, 4, 2, 1>;       // 64 x 128, 4 waves of 64 x 32: up to 64 tokens
+using Small = Shape<1, 4, 2, 1, 4>;    // 64 x 128, 4 waves of 64 x 32: up to 64 tokens, bound by the loads of w
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
 // What the rows with a target need, in their order (padded with zeros to a
 // multiple of 256 rows).
 struct Rows {
-    int32_t* count;        // [1]
+    int32_t* count;        // [3]: the rows; backward: a piece's width, workgroups that share a tile of dx
     float* most;           // [1]: the largest |dloss|, |dlse| (1 where that is 0 or not finite)
     int32_t* place;        // [T]: a token's row, -1 without a target
     int32_t* token;        // [Tp]
@@ -55,10 +58,45 @@ __device__ __forceinline__ int target_of(const void* targets, int wide, int64_t 
     return v >= 0 && v < V ? (int)v : -1;
 }
 
+// How the backward pass is cut, from the number of rows.
+struct Cut {
+    int64_t V, room;       // values of dz that the workspace holds
+    int bm, tiles_n;       // rows a tile of dx, tiles along its width
+    int slots, most;       // tiles' sums that the workspace holds, workgroups a tile at most
+    int cus;
+};
+
+__host__ __device__ inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+__host__ __device__ inline int64_t piece_width(const Cut& c, int64_t rows)
+{
+    const int64_t fits = c.room / up(rows > 0 ? rows : 1, 256) / 256 * 256;
+    return fits < up(c.V, 256) ? fits : up(c.V, 256);
+}
+
+// Workgroups that share a tile of dx, each a part of the piece: the fewest
+// microseconds.  A step of 64 values takes a compute unit 1.9 us per 256 x 256
+// (measured: 1.15 PFLOP/s); a part's sums are read and written again, 0.117 us
+// of the chip's time (512 KiB at 4.5 TB/s).
+// (By the 64 lanes of a wave.)
+__device__ inline int dx_splits(const Cut& c, int64_t rows, int64_t width)
+{
+    const int n = (int)((rows + c.bm - 1) / c.bm) * c.tiles_n;
+    const float size = c.bm / 256.0f * (c.bm / 256.0f);
+    uint64_t best = ~0ull;             // the time's bits (no float here is negative) and the number
+    for (int s = 1 + (threadIdx.x & 63); s <= c.most && (s == 1 || n * s <= c.slots); s += 64) {
+        const float t = (float)((n * s + c.cus - 1) / c.cus) * (width / (float)s * 0.0292f * size + 3.0f) + n * s * 0.117f * size;
+        best = min(best, (uint64_t)as_u32(t) << 32 | (uint32_t)s);
+    }
+    for (int m = 1; m < 64; m *= 2) best = min(best, (uint64_t)__shfl_xor((unsigned long long)best, m));
+    return (int)best;
+}
+
 // One workgroup lists the rows with a target.
 __global__ __launch_bounds__(1024) void ce_rows_kernel(const void* targets, int wide, int64_t T, int64_t V, Rows r,
-                                                       const float* dloss, const float* dlse, const float* lse)
+                                                       const float* dloss, const float* dlse, const float* lse, Cut cut)
 {
+    const bool backward = cut.V > 0;       // (dloss of no tokens may be a null pointer)
     __shared__ int s_count[16];
     __shared__ float s_top[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -84,7 +122,7 @@ __global__ __launch_bounds__(1024) void ce_rows_kernel(const void* targets, int 
         if (target >= 0) {
             r.token[at] = (int)t;
             r.target[at] = target;
-            if (dloss) {
+            if (backward) {
                 const float b = dloss[t], e = dlse ? dlse[t] : 0.0f;
                 r.dloss[at] = b;
                 r.dlse[at] = e;
@@ -98,18 +136,23 @@ __global__ __launch_bounds__(1024) void ce_rows_kernel(const void* targets, int 
     for (int i = before + threadIdx.x; i < padded; i += 1024) {
         r.token[i] = 0;
         r.target[i] = -1;
-        if (dloss) r.dloss[i] = r.dlse[i] = r.lse[i] = 0.0f;
+        if (backward) r.dloss[i] = r.dlse[i] = r.lse[i] = 0.0f;
     }
-    if (dloss) {
+    if (backward) {
         if (bad) top = INFINITY;
         for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
         if (lane == 0) s_top[wave] = top;
         __syncthreads();
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s_top[i]);
     }
-    if (threadIdx.x == 0) {
-        *r.count = before;
-        if (dloss) *r.most = top > 0.0f && top < INFINITY ? top : 1.0f;
+    if (wave != 0) return;
+    const int64_t width = backward ? piece_width(cut, before) : 0;
+    const int splits = backward ? dx_splits(cut, before, width) : 0;
+    if (lane == 0) {
+        r.count[0] = before;
+        r.count[1] = (int)width;
+        r.count[2] = splits;
+        if (backward) *r.most = top > 0.0f && top < INFINITY ? top : 1.0f;
     }
 }
 
@@ -139,28 +182,27 @@ __global__ __launch_bounds__(256) void ce_gather_kernel(const uint16_t* x, int64
 // ------------------------------------------------------------------------
 struct ScoreArgs {
     const uint16_t *x, *w;
-    int64_t ldx, ldw, T, V, v0;        // the vocabulary from v0 on
-    int K, tiles_n;
+    int64_t ldx, ldw, T, V;
+    int K, tiles_n;                    // tiles along the vocabulary (forward)
+    int piece;                         // of the vocabulary (backward)
     const void* targets;               // the forward pass without a list of rows
     int wide;
     Rows r;                            // r.count nullptr: every token is a row
     int64_t Tp;
     float2* part;                      // [tiles_n][Tp]
     float* z_target;                   // [Tp]
-    uint16_t* dz;                      // [Tp][ldz] (backward)
-    int64_t ldz;
+    uint16_t* dz;                      // [rows][a piece's width] (backward)
 };
 
 template <class S>
-__device__ __forceinline__ bool score_tile(const ScoreArgs& p, f32x16 (&acc)[S::TI][S::TJ], int64_t& rows, int64_t& m0,
-                                           int64_t& n0, int& tn, char* smem)
+__device__ __forceinline__ bool score_tile(const ScoreArgs& p, f32x16 (&acc)[S::TI][S::TJ], int64_t& rows, int64_t v0,
+                                           int tiles_n, int64_t& m0, int64_t& n0, int& tn, char* smem)
 {
-    rows = p.r.count ? *p.r.count : p.T;
     const int tiles_m = (int)((rows + S::BM - 1) / S::BM);
-    if ((int64_t)blockIdx.x >= (int64_t)tiles_m * p.tiles_n) return false;
+    if ((int64_t)blockIdx.x >= (int64_t)tiles_m * tiles_n) return false;
     int tm;
-    tile_of(blockIdx.x, tiles_m, p.tiles_n, tm, tn);
-    m0 = (int64_t)tm * S::BM, n0 = p.v0 + (int64_t)tn * S::BN;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    m0 = (int64_t)tm * S::BM, n0 = v0 + (int64_t)tn * S::BN;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Loader<ALONG, S::BM, S::NW> la;
     Loader<ALONG, S::BN, S::NW> lb;
@@ -179,9 +221,9 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_score_kernel(ScoreArgs p)
 {
     extern __shared__ __align__(256) char smem[];
     f32x16 acc[S::TI][S::TJ];
-    int64_t rows, m0, n0;
+    int64_t rows = p.r.count ? *p.r.count : p.T, m0, n0;
     int tn;
-    if (!score_tile<S>(p, acc, rows, m0, n0, tn, smem)) return;
+    if (!score_tile<S>(p, acc, rows, 0, p.tiles_n, m0, n0, tn, smem)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int wm = wave / S::NWN, wn = wave % S::NWN;
     const int64_t nw = n0 + wn * S::WN;
@@ -280,6 +322,21 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(ScoreArgs p, float* loss,
 // Backward
 // ------------------------------------------------------------------------
 
+// A piece of the vocabulary: words v0 .. v0 + width - 1, padded to a multiple of
+// 256 columns of dz, whose rows are ld apart; none where v0 is past the last.
+struct Piece {
+    int64_t v0, width, padded, ld;
+};
+__device__ __forceinline__ Piece piece_of(const Rows& r, int piece, int64_t V)
+{
+    Piece p;
+    p.ld = r.count[1];
+    p.v0 = piece * p.ld;
+    p.width = min(p.ld, max(V - p.v0, (int64_t)0));
+    p.padded = up(p.width, 256);
+    return p;
+}
+
 // A tile's values as BF16 through LDS, so that whole rows are written: f(i, j,
 // k) is the lane's value, write(row, chunk) where 16 bytes of the tile go, or
 // nullptr.  16-byte chunk c of row r sits in slot c ^ (r % 32).
@@ -317,9 +374,10 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_gradient_kernel(ScoreArgs p)
 {
     extern __shared__ __align__(256) char smem[];
     f32x16 acc[S::TI][S::TJ];
-    int64_t rows, m0, n0;
+    const Piece at = piece_of(p.r, p.piece, p.V);
+    int64_t rows = p.r.count[0], m0, n0;
     int tn;
-    if (!score_tile<S>(p, acc, rows, m0, n0, tn, smem)) return;
+    if (!score_tile<S>(p, acc, rows, at.v0, (int)(at.padded / S::BN), m0, n0, tn, smem)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int wm = wave / S::NWN, wn = wave % S::NWN;
     const int64_t nw = n0 + wn * S::WN;
@@ -340,93 +398,88 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_gradient_kernel(ScoreArgs p)
             }
     }
     store_tile<S>(smem, [&](int i, int j, int k) { return acc[i][j][k]; },
-                  [&](int row, int c) { return p.dz + (m0 + row) * p.ldz + (n0 - p.v0) + 8 * c; });
+                  [&](int row, int c) { return p.dz + (m0 + row) * at.ld + (n0 - at.v0) + 8 * c; });
 }
 
 struct GradArgs {
     const uint16_t *dz, *w, *xc;
-    int64_t ldz, ldw, V, v0, width;    // width: vocabulary of the piece, padded to 256
-    int K, tiles_n, tiles_m, splits, first;
-    int64_t per;                       // contraction values a split (dx)
+    int64_t ldw, V;
+    int K, piece, tiles_n;             // tiles along dx's width
     Rows r;
-    float* sums;                       // [splits][tiles_m][tiles_n][BM x BN]
+    float* sums;                       // [slots][bm x 256 (128)]
     uint16_t *dx, *dw;
 };
 
-// dx += dz w over the piece's vocabulary, or a split of it; the sums stay in
+// dx += dz w over the piece's vocabulary, or a part of it; the sums stay in
 // the accumulators' order.
 template <class S>
 __global__ __launch_bounds__(S::THREADS, 1) void ce_dx_kernel(GradArgs p)
 {
     extern __shared__ __align__(256) char smem[];
-    const int64_t rows = *p.r.count;
-    const int tiles_m = (int)((rows + S::BM - 1) / S::BM);
+    const Piece at = piece_of(p.r, p.piece, p.V);
+    const int64_t rows = p.r.count[0];
+    const int splits = p.r.count[2], tiles_m = (int)((rows + S::BM - 1) / S::BM);
     const int64_t each = (int64_t)tiles_m * p.tiles_n;
-    if ((int64_t)blockIdx.x >= each * p.splits) return;
+    if (at.width == 0 || (int64_t)blockIdx.x >= each * splits) return;
     const int split = (int)(blockIdx.x / each);
     int tm, tn;
     tile_of(blockIdx.x - split * each, tiles_m, p.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * S::BM, n0 = (int64_t)tn * S::BN, k0 = split * p.per;
+    const int64_t per = up((at.padded + splits - 1) / splits, BK);
+    const int64_t m0 = (int64_t)tm * S::BM, n0 = (int64_t)tn * S::BN, k0 = split * per;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t values = max((int64_t)0, min(p.per, min(p.width, p.V - p.v0) - k0));
+    const int64_t values = max((int64_t)0, min(per, at.width - k0));
     Loader<ALONG, S::BM, S::NW> la;
     Loader<ACROSS, S::BN, S::NW> lb;
-    la.rows([&](int r) { return p.dz + (m0 + r) * p.ldz + k0; }, wave, lane);
-    lb.columns(p.w + min(p.v0 + k0, p.V - 1) * p.ldw, p.ldw, n0, p.K, wave, lane);
+    la.rows([&](int r) { return p.dz + (m0 + r) * at.ld + k0; }, wave, lane);
+    lb.columns(p.w + min(at.v0 + k0, p.V - 1) * p.ldw, p.ldw, n0, p.K, wave, lane);
     f32x16 acc[S::TI][S::TJ];
     product<S, ALONG, ACROSS>(acc, la, lb, values, smem);
-    float4* sums = reinterpret_cast<float4*>(p.sums) +
-                   (((int64_t)split * p.tiles_m + tm) * p.tiles_n + tn) * (S::BM * S::BN / 4) + threadIdx.x;
+    float4* sums = reinterpret_cast<float4*>(p.sums) + ((int64_t)(tm * p.tiles_n + tn) * splits + split) * (S::BM * S::BN / 4) + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < S::TI; ++i)
 #pragma unroll
         for (int j = 0; j < S::TJ; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                float4* at = sums + ((i * S::TJ + j) * 4 + g) * S::THREADS;
+                float4* to = sums + ((i * S::TJ + j) * 4 + g) * S::THREADS;
                 float4 v = make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-                if (!p.first) {
-                    const float4 o = *at;
+                if (p.piece > 0) {
+                    const float4 o = *to;
                     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                 }
-                *at = v;
+                *to = v;
             }
 }
 
-// The splits' sums to the tokens' rows of dx.
+// The parts' sums to the tokens' rows of dx.  A thread takes two of a lane's
+// groups of 4 columns, which the lane halves swap so that each writes 16 bytes.
 template <class S>
-__global__ __launch_bounds__(S::THREADS, 1) void ce_dx_store_kernel(GradArgs p)
+__global__ __launch_bounds__(256) void ce_dx_store_kernel(GradArgs p)
 {
-    extern __shared__ __align__(256) char smem[];
-    const int64_t rows = *p.r.count;
-    const int tm = blockIdx.x / p.tiles_n, tn = blockIdx.x % p.tiles_n;
-    const int64_t m0 = (int64_t)tm * S::BM, n0 = (int64_t)tn * S::BN;
+    constexpr int PAIRS = S::TI * S::TJ * 2, PER = S::BM * S::BN / 4;      // pairs of groups a lane, float4 a tile
+    const int64_t rows = p.r.count[0];
+    const int splits = p.r.count[2];
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t tile = e / (PAIRS * S::THREADS);
+    const int64_t m0 = tile / p.tiles_n * S::BM, n0 = tile % p.tiles_n * S::BN;
     if (m0 >= rows) return;
-    const float scale = *p.r.most;
-    f32x16 acc[S::TI][S::TJ];
-#pragma unroll
-    for (int i = 0; i < S::TI; ++i)
-#pragma unroll
-        for (int j = 0; j < S::TJ; ++j) acc[i][j] = f32x16{};
-    for (int s = 0; s < p.splits; ++s) {
-        const float4* sums = reinterpret_cast<const float4*>(p.sums) +
-                             (((int64_t)s * p.tiles_m + tm) * p.tiles_n + tn) * (S::BM * S::BN / 4) + threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < S::TI; ++i)
-#pragma unroll
-            for (int j = 0; j < S::TJ; ++j)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float4 v = sums[((i * S::TJ + j) * 4 + g) * S::THREADS];
-                    acc[i][j][4 * g] += v.x, acc[i][j][4 * g + 1] += v.y;
-                    acc[i][j][4 * g + 2] += v.z, acc[i][j][4 * g + 3] += v.w;
-                }
+    const int in = (int)(e % (PAIRS * S::THREADS)), pair = in / S::THREADS, thread = in % S::THREADS;
+    const int lane = thread & 63, wave = thread >> 6, half = lane >> 5;
+    const float4* sums = reinterpret_cast<const float4*>(p.sums) + tile * splits * PER + 2 * pair * S::THREADS + thread;
+    float4 a = {}, b = {};
+    for (int s = 0; s < splits; ++s) {
+        const float4 u = sums[(int64_t)s * PER], v = sums[(int64_t)s * PER + S::THREADS];
+        a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+        b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
     }
-    store_tile<S>(smem, [&](int i, int j, int k) { return acc[i][j][k] * scale; },
-                  [&](int row, int c) -> uint16_t* {
-                      if (m0 + row >= rows || n0 + 8 * c >= p.K) return nullptr;
-                      return p.dx + (int64_t)p.r.token[m0 + row] * p.K + n0 + 8 * c;
-                  });
+    const float scale = *p.r.most;
+    const auto lo = __builtin_amdgcn_permlane32_swap(bf16x2_rne(a.x * scale, a.y * scale), bf16x2_rne(b.x * scale, b.y * scale), false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap(bf16x2_rne(a.z * scale, a.w * scale), bf16x2_rne(b.z * scale, b.w * scale), false, false);
+    const int i = pair / 2 / S::TJ, j = pair / 2 % S::TJ, g = 2 * (pair & 1);
+    const int64_t row = m0 + wave / S::NWN * S::WM + 32 * i + (lane & 31);
+    const int64_t col = n0 + wave % S::NWN * S::WN + 32 * j + 8 * (g + half);
+    if (row < rows && col < p.K)
+        *reinterpret_cast<uint4*>(p.dx + (int64_t)p.r.token[row] * p.K + col) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
 }
 
 // The piece's rows of dw = dz^T x.
@@ -434,33 +487,36 @@ template <class S>
 __global__ __launch_bounds__(S::THREADS, 1) void ce_dw_kernel(GradArgs p)
 {
     extern __shared__ __align__(256) char smem[];
-    const int64_t rows = *p.r.count;
+    const Piece at = piece_of(p.r, p.piece, p.V);
+    const int64_t rows = p.r.count[0];
+    const int tiles_m = (int)(at.padded / S::BM), tiles_n = (p.K + S::BN - 1) / S::BN;
+    if ((int64_t)blockIdx.x >= (int64_t)tiles_m * tiles_n) return;
     int tm, tn;
-    tile_of(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = (int64_t)tm * S::BM, n0 = (int64_t)tn * S::BN;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Loader<ACROSS, S::BM, S::NW> la;
     Loader<ACROSS, S::BN, S::NW> lb;
-    la.columns(p.dz, p.ldz, m0, p.ldz, wave, lane);
+    la.columns(p.dz, at.ld, m0, at.ld, wave, lane);
     lb.columns(p.xc, p.K, n0, p.K, wave, lane);
     f32x16 acc[S::TI][S::TJ];
-    product<S, ACROSS, ACROSS>(acc, la, lb, (rows + BK - 1) / BK * BK, smem);
+    product<S, ACROSS, ACROSS>(acc, la, lb, up(rows, BK), smem);
     const float scale = *p.r.most;
     store_tile<S>(smem, [&](int i, int j, int k) { return acc[i][j][k] * scale; },
                   [&](int row, int c) -> uint16_t* {
-                      const int64_t v = p.v0 + m0 + row;
-                      if (v >= p.V || m0 + row >= p.width || n0 + 8 * c >= p.K) return nullptr;
-                      return p.dw + v * p.K + n0 + 8 * c;
+                      if (m0 + row >= at.width || n0 + 8 * c >= p.K) return nullptr;
+                      return p.dw + (at.v0 + m0 + row) * p.K + n0 + 8 * c;
                   });
 }
 
 // Up to 64 tokens the rows of a 256 x 256 tile would be padding for the most
 // part, and its 8 waves would wait for one tile's loads.
 constexpr int64_t SMALL = 64;
-// dz of one piece of the vocabulary: 256 MiB at most where that is 8192 wide or more.
+// dz of one piece of the vocabulary: 256 MiB, or 8192 words where that is more.
 constexpr int64_t PIECE_VALUES = (int64_t)1 << 27, PIECE_LEAST = 8192;
-
-int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+// Parts of dx: sums of 1280 tiles at most, where their number is not more
+// already, and 1024 values of the contraction each at least.
+constexpr int64_t SLOTS = 1280, PART_LEAST = 1024;
 
 // The workspace's parts, each at a multiple of 256 bytes.
 struct Layout {
@@ -477,10 +533,11 @@ struct Layout {
 
 struct Plan {
     Rows r{};
-    int64_t Tp, piece = 0;
+    int64_t Tp;
     bool small, list;
-    int tiles_n = 0, splits = 1, dx_m = 0, dx_n = 0;
-    int64_t per = 0;
+    int tiles_n = 0;                   // forward
+    Cut cut{};                         // backward
+    int pieces = 0;
     float2* part = nullptr;
     float *z_target = nullptr, *sums = nullptr;
     uint16_t *xc = nullptr, *dz = nullptr;
@@ -492,32 +549,35 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool backward, void* workspace)
     Plan p;
     Layout at(workspace);
     p.small = T <= SMALL;
+    const int bm = p.small ? Small::BM : Big::BM, bn = p.small ? Small::BN : Big::BN;
     p.Tp = up(std::max<int64_t>(T, 1), 256);
     // the forward pass of one tile of tokens gains nothing from a list of rows
     p.list = backward || T > Big::BM;
     if (p.list) {
-        p.r.count = at.take<int32_t>(1);
+        p.r.count = at.take<int32_t>(3);
         p.r.most = at.take<float>(1);
         p.r.place = at.take<int32_t>(p.Tp);
         p.r.token = at.take<int32_t>(p.Tp);
         p.r.target = at.take<int32_t>(p.Tp);
     }
     if (!backward) {
-        p.tiles_n = (int)(up(V, p.small ? Small::BN : Big::BN) / (p.small ? Small::BN : Big::BN));
+        p.tiles_n = (int)(up(V, bn) / bn);
         p.part = at.take<float2>(p.tiles_n * p.Tp);
         p.z_target = at.take<float>(p.Tp);
     } else {
         p.r.lse = at.take<float>(p.Tp), p.r.dloss = at.take<float>(p.Tp), p.r.dlse = at.take<float>(p.Tp);
         p.xc = at.take<uint16_t>(p.Tp * K);
-        p.piece = std::min(up(V, 256), std::max(PIECE_VALUES / p.Tp / 256 * 256, PIECE_LEAST));
-        p.dz = at.take<uint16_t>(p.Tp * p.piece);
-        const int bm = p.small ? Small::BM : Big::BM, bn = p.small ? Small::BN : Big::BN;
-        p.dx_m = (int)(up(std::max<int64_t>(T, 1), bm) / bm), p.dx_n = (int)(up(K, bn) / bn);
-        // few tiles of dx: the vocabulary is split over workgroups, 1024 values each at least
-        const int64_t tiles = (int64_t)p.dx_m * p.dx_n;
-        p.splits = (int)std::max<int64_t>(1, std::min(512 / tiles, p.piece / 1024));
-        p.per = up((p.piece + p.splits - 1) / p.splits, BK);
-        p.sums = at.take<float>(p.splits * tiles * bm * bn);
+        Cut& c = p.cut;
+        c.V = V;
+        // (all of the vocabulary for any number of rows, where that is less)
+        c.room = std::min(p.Tp * up(V, 256), std::max(PIECE_VALUES, p.Tp * PIECE_LEAST));
+        p.pieces = (int)((V + piece_width(c, p.Tp) - 1) / piece_width(c, p.Tp));
+        p.dz = at.take<uint16_t>(c.room);
+        c.bm = bm, c.tiles_n = (int)(up(K, bn) / bn);
+        const int64_t tiles = up(std::max<int64_t>(T, 1), bm) / bm * c.tiles_n;
+        c.most = (int)std::max<int64_t>(1, up(V, 256) / PART_LEAST);
+        c.slots = (int)std::max(tiles, std::min(SLOTS, tiles * c.most));
+        p.sums = at.take<float>((int64_t)c.slots * bm * bn);
     }
     p.bytes = at.bytes;
     return p;
@@ -526,7 +586,6 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool backward, void* workspace)
 template <class S, class A>
 hipError_t go(void (*kernel)(A), int64_t grid, const A& a, hipStream_t stream)
 {
-    if (grid == 0) return hipSuccess;
     constexpr int LDS = std::max(S::LDS, 2 * S::BM * S::BN);       // the stages, then the tile on its way out
     if (LDS > 64 * 1024)
         if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
@@ -556,7 +615,7 @@ hipError_t launch_cross_entropy_fwd(const CrossEntropyArgs& c, hipStream_t strea
 {
     const Plan p = make_plan(c.T, c.V, c.K, false, c.workspace);
     const ScoreArgs s = score_args(c, p);
-    if (p.list) ce_rows_kernel<<<1, 1024, 0, stream>>>(c.targets, c.wide, c.T, c.V, p.r, nullptr, nullptr, nullptr);
+    if (p.list) ce_rows_kernel<<<1, 1024, 0, stream>>>(c.targets, c.wide, c.T, c.V, p.r, nullptr, nullptr, nullptr, p.cut);
     hipError_t e = p.small ? go<Small>(ce_score_kernel<Small>, p.tiles_n, s, stream)
                            : go<Big>(ce_score_kernel<Big>, p.Tp / Big::BM * p.tiles_n, s, stream);
     if (e != hipSuccess) return e;
@@ -564,38 +623,42 @@ hipError_t launch_cross_entropy_fwd(const CrossEntropyArgs& c, hipStream_t strea
     return hipGetLastError();
 }
 
-hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& c, hipStream_t stream)
+template <class S>
+static hipError_t backward(const CrossEntropyArgs& c, Plan& p, hipStream_t stream)
 {
-    const Plan p = make_plan(c.T, c.V, c.K, true, c.workspace);
+    int device;
+    if (hipError_t e = hipGetDevice(&device); e != hipSuccess) return e;
+    if (hipError_t e = hipDeviceGetAttribute(&p.cut.cus, hipDeviceAttributeMultiprocessorCount, device); e != hipSuccess) return e;
     ScoreArgs s = score_args(c, p);
-    ce_rows_kernel<<<1, 1024, 0, stream>>>(c.targets, c.wide, c.T, c.V, p.r, c.dloss, c.dlse, c.lse);
+    ce_rows_kernel<<<1, 1024, 0, stream>>>(c.targets, c.wide, c.T, c.V, p.r, c.dloss, c.dlse, c.lse, p.cut);
     ce_gather_kernel<<<(uint32_t)(c.T + 256), 256, 0, stream>>>(s.x, c.ldx, c.T, (int)c.K, p.r, p.xc, static_cast<uint16_t*>(c.dx));
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     s.x = p.xc, s.ldx = c.K, s.r.token = nullptr;
-    s.dz = p.dz, s.ldz = p.piece;
+    s.dz = p.dz;
     GradArgs g{};
-    g.dz = p.dz, g.w = s.w, g.xc = p.xc, g.ldz = p.piece, g.ldw = c.ldw, g.V = c.V, g.K = (int)c.K;
-    g.splits = p.splits, g.per = p.per, g.r = p.r, g.sums = p.sums;
+    g.dz = p.dz, g.w = s.w, g.xc = p.xc, g.ldw = c.ldw, g.V = c.V, g.K = (int)c.K;
+    g.tiles_n = p.cut.tiles_n, g.r = p.r, g.sums = p.sums;
     g.dx = static_cast<uint16_t*>(c.dx), g.dw = static_cast<uint16_t*>(c.dw);
-    for (int64_t v0 = 0; v0 < c.V; v0 += p.piece) {
-        const int64_t width = up(std::min(p.piece, c.V - v0), 256);
-        s.v0 = g.v0 = v0, g.width = width;
-        g.first = v0 == 0;
-        s.tiles_n = (int)(width / (p.small ? Small::BN : Big::BN));
-        hipError_t e = p.small ? go<Small>(ce_gradient_kernel<Small>, s.tiles_n, s, stream)
-                               : go<Big>(ce_gradient_kernel<Big>, p.Tp / Big::BM * s.tiles_n, s, stream);
-        if (e != hipSuccess) return e;
-        g.tiles_m = p.dx_m, g.tiles_n = p.dx_n;
-        const int64_t grid = (int64_t)p.dx_m * p.dx_n * p.splits;
-        e = p.small ? go<Small>(ce_dx_kernel<Small>, grid, g, stream) : go<Big>(ce_dx_kernel<Big>, grid, g, stream);
-        if (e != hipSuccess) return e;
-        g.tiles_m = (int)(width / Big::BM), g.tiles_n = (int)(up(c.K, Big::BN) / Big::BN);
-        if ((e = go<Big>(ce_dw_kernel<Big>, (int64_t)g.tiles_m * g.tiles_n, g, stream)) != hipSuccess) return e;
+    // grids for any number of rows; workgroups without a tile end at once
+    const int64_t words = up(c.V, 256), tiles_m = up(std::max<int64_t>(c.T, 1), S::BM) / S::BM;
+    const int64_t scores = std::min(tiles_m * (words / S::BN), (p.cut.room + (int64_t)S::BM * S::BN - 1) / (S::BM * S::BN));
+    for (int i = 0; i < p.pieces; ++i) {
+        s.piece = g.piece = i;
+        if (hipError_t e = go<S>(ce_gradient_kernel<S>, scores, s, stream); e != hipSuccess) return e;
+        if (hipError_t e = go<S>(ce_dx_kernel<S>, p.cut.slots, g, stream); e != hipSuccess) return e;
+        // (the first piece may be all of the vocabulary, a later one is no wider than the rest)
+        const int64_t rest = up(c.V - i * piece_width(p.cut, p.Tp), 256);
+        if (hipError_t e = go<Big>(ce_dw_kernel<Big>, rest / Big::BM * (up(c.K, Big::BN) / Big::BN), g, stream); e != hipSuccess) return e;
     }
     if (c.T == 0) return hipSuccess;
-    g.tiles_m = p.dx_m, g.tiles_n = p.dx_n;
-    const int64_t grid = (int64_t)p.dx_m * p.dx_n;
-    return p.small ? go<Small>(ce_dx_store_kernel<Small>, grid, g, stream) : go<Big>(ce_dx_store_kernel<Big>, grid, g, stream);
+    ce_dx_store_kernel<S><<<(uint32_t)(tiles_m * g.tiles_n * (S::BM * S::BN / 8 / 256)), 256, 0, stream>>>(g);
+    return hipGetLastError();
+}
+
+hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& c, hipStream_t stream)
+{
+    Plan p = make_plan(c.T, c.V, c.K, true, c.workspace);
+    return p.small ? backward<Small>(c, p, stream) : backward<Big>(c, p, stream);
 }
 
 } // namespace fgs

@@ -4,12 +4,14 @@
 //
 // A workgroup of NWM x NWN waves owns a BM x BN tile of C, each wave TI x TJ
 // accumulators of 32 x 32.  The contraction advances in steps of 64 values,
-// staged in LDS by copies that pass no register, two stages in turn.  An
+// staged in LDS by copies that pass no register, into a ring of stages.  An
 // operand whose contraction runs along its rows is staged as BM (or BN) rows
 // of 128 bytes and read 16 bytes a lane; one whose contraction runs across its
 // rows as 64 rows of BM (or BN) values, read by the transposing loads, so no
 // operand has to be transposed in memory first.
 #pragma once
+
+#include <type_traits>
 
 #include "fgs_device.h"
 #include "operators_internal.h"
@@ -29,13 +31,14 @@ constexpr int BK = 64;                       // contraction values a stage
 
 enum Side { ALONG, ACROSS };                 // the contraction runs along an operand's rows, or across them
 
-template <int NWM_, int NWN_, int TI_, int TJ_>
+template <int NWM_, int NWN_, int TI_, int TJ_, int STAGES_ = 2>
 struct Shape {
-    static constexpr int NWM = NWM_, NWN = NWN_, TI = TI_, TJ = TJ_;
+    static constexpr int NWM = NWM_, NWN = NWN_, TI = TI_, TJ = TJ_, STAGES = STAGES_;
+    static_assert((STAGES & (STAGES - 1)) == 0, "a stage's place is its number's low bits");
     static constexpr int NW = NWM * NWN, THREADS = 64 * NW;
     static constexpr int WM = 32 * TI, WN = 32 * TJ;                 // a wave's part of the tile
     static constexpr int BM = WM * NWM, BN = WN * NWN;
-    static constexpr int A_BYTES = BM * BK * 2, STAGE = (BM + BN) * BK * 2, LDS = 2 * STAGE;
+    static constexpr int A_BYTES = BM * BK * 2, STAGE = (BM + BN) * BK * 2, LDS = STAGES * STAGE;
 };
 
 // The lane halves of a 32x32 accumulator tile: register i of lane l holds
@@ -68,9 +71,13 @@ __device__ __forceinline__ void g2lds16(const char* at, uint32_t lds_addr)
                  :: "v"(at), "s"(lds_addr) : "memory", "m0");
 }
 
-// This wave's copies have landed and its LDS reads are done, and so for every
-// other wave of the workgroup.
-__device__ __forceinline__ void publish() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All but the last LEFT of this wave's copies have landed and its LDS reads are
+// done, and so for every other wave of the workgroup.
+template <int LEFT>
+__device__ __forceinline__ void publish()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(LEFT) : "memory");
+}
 
 // 16-byte chunk c of staged row r sits in slot c ^ f(r): 16 rows of one chunk
 // (ALONG), or 4 rows of 4 neighbouring chunks (ACROSS), touch every bank once.
@@ -113,21 +120,18 @@ struct Loader {
             at[j] = reinterpret_cast<const char*>(base) + row(wave, lane, j) * ld +
                     2 * min(first + 8 * chunk(wave, lane, j), width - 8);
     }
-    // the next stage; ACROSS: `left` rows are there, later ones repeat the last
-    __device__ __forceinline__ void issue(uint32_t lds, int64_t left, int wave, int lane)
+    // copy j of the next stage
+    __device__ __forceinline__ void issue(int j, uint32_t lds, int wave)
     {
+        g2lds16(at[j], lds + (wave * N + j) * 1024);
+        at[j] += SIDE == ALONG ? 2 * BK : BK * ld;
+    }
+    // the next stage is the last and has only `left` rows (ACROSS): later ones repeat the last
+    __device__ __forceinline__ void shorten(int left, int wave, int lane)
+    {
+        if constexpr (SIDE == ACROSS) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const uint32_t to = lds + (wave * N + j) * 1024;
-            if constexpr (SIDE == ALONG) {
-                g2lds16(at[j], to);
-                at[j] += 2 * BK;
-            } else {
-                const char* from = at[j];
-                if (left < BK) from -= max((int64_t)0, row(wave, lane, j) - (left - 1)) * ld;
-                g2lds16(from, to);
-                at[j] += BK * ld;
-            }
+            for (int j = 0; j < N; ++j) at[j] -= max(0, row(wave, lane, j) - (left - 1)) * ld;
         }
     }
 };
@@ -184,41 +188,72 @@ __device__ __forceinline__ void product(f32x16 (&acc)[S::TI][S::TJ], Loader<SA, 
     for (int j = 0; j < S::TJ; ++j) ab[j] = fragment_address<SB, S::BN>(wn * S::WN + 32 * j, lane);
 
     bf16x8 fa[2][S::TI], fb[2][S::TJ];
-    auto read = [&](int set, uint32_t stage, int ks) {
-#pragma unroll
-        for (int i = 0; i < S::TI; ++i) fa[set][i] = fragment<SA, S::BM>(aa[i], stage, ks);
-#pragma unroll
-        for (int j = 0; j < S::TJ; ++j) fb[set][j] = fragment<SB, S::BN>(ab[j], stage + S::A_BYTES, ks);
+    constexpr int READS = S::TI + S::TJ, MMAS = S::TI * S::TJ;
+    constexpr int AHEAD = S::STAGES - 1, A_COPIES = Loader<SA, S::BM, S::NW>::N, COPIES = A_COPIES + Loader<SB, S::BN, S::NW>::N;
+    auto place = [&](int step) { return lds + (step & (S::STAGES - 1)) * S::STAGE; };
+    auto read = [&](int f, int set, uint32_t stage, int ks) {
+        if (f < S::TI) fa[set][f] = fragment<SA, S::BM>(aa[f], stage, ks);
+        else fb[set][f - S::TI] = fragment<SB, S::BN>(ab[f - S::TI], stage + S::A_BYTES, ks);
     };
-    auto multiply = [&](int set) {
-#pragma unroll
-        for (int i = 0; i < S::TI; ++i)
-#pragma unroll
-            for (int j = 0; j < S::TJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+    auto multiply = [&](int t, int set) {
+        const int i = t / S::TJ, j = t % S::TJ;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
     };
-    la.issue(lds, values, wave, lane);
-    lb.issue(lds + S::A_BYTES, values, wave, lane);
-    publish();
-    read(0, lds, 0);
-    for (int step = 0; step < steps; ++step) {
-        const uint32_t here = lds + (step & 1) * S::STAGE, next = lds + ((step & 1) ^ 1) * S::STAGE;
-        const bool more = step + 1 < steps;
-        if (more) {      // every wave is past its reads of the other stage
-            const int64_t left = values - (int64_t)(step + 1) * BK;
-            la.issue(next, left, wave, lane);
-            lb.issue(next + S::A_BYTES, left, wave, lane);
+    const int last = (int)(values - (int64_t)(steps - 1) * BK);       // values of the last stage
+    auto copy = [&](int c, int step) {
+        if (c == 0 && step == steps - 1 && last < BK) {
+            la.shorten(last, wave, lane);
+            lb.shorten(last, wave, lane);
         }
+        if (c < A_COPIES) la.issue(c, place(step), wave);
+        else lb.issue(c - A_COPIES, place(step) + S::A_BYTES, wave);
+    };
 #pragma unroll
-        for (int ks = 0; ks < 3; ++ks) {
-            read((ks + 1) & 1, here, ks + 1);
-            multiply(ks & 1);
-        }
+    for (int step = 0; step < AHEAD; ++step)
+        if (step < steps)
+#pragma unroll
+            for (int c = 0; c < COPIES; ++c) copy(c, step);
+    if (AHEAD > 1 && steps >= AHEAD) publish<(AHEAD - 1) * COPIES>();
+    else publish<0>();
+#pragma unroll
+    for (int f = 0; f < READS; ++f) read(f, 0, lds, 0);
+    // The order below is kept as it is written: a fragment is read a whole
+    // k-step before its products, and a copy starts beside a product, so that
+    // neither is waited for (left to the compiler, reads stand right before
+    // their products).
+    // fill: the stage AHEAD of this one is copied, every wave being past its
+    // reads of the place; more: there is a next stage
+    auto advance = [&](int step, auto fill, auto more) {
+#pragma unroll
+        for (int ks = 0; ks < 3; ++ks)
+#pragma unroll
+            for (int t = 0; t < MMAS; ++t) {
+                multiply(t, ks & 1);
+#pragma unroll
+                for (int f = t * READS / MMAS; f < (t + 1) * READS / MMAS; ++f) read(f, (ks + 1) & 1, place(step), ks + 1);
+                if constexpr (fill) {
+                    if (ks == 0)
+#pragma unroll
+                        for (int c = t * COPIES / MMAS; c < (t + 1) * COPIES / MMAS; ++c) copy(c, step + AHEAD);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         // the stage's last products run after the barrier, beside the next stage's first reads
-        publish();
-        if (more) read(0, next, 0);
-        multiply(1);
-    }
+        publish<fill ? (AHEAD - 1) * COPIES : 0>();
+#pragma unroll
+        for (int t = 0; t < MMAS; ++t) {
+            multiply(t, 1);
+            if constexpr (more) {
+#pragma unroll
+                for (int f = t * READS / MMAS; f < (t + 1) * READS / MMAS; ++f) read(f, 0, place(step + 1), 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int step = 0;
+    for (; step < steps - AHEAD; ++step) advance(step, std::true_type{}, std::true_type{});
+    for (; step < steps - 1; ++step) advance(step, std::false_type{}, std::true_type{});
+    advance(step, std::false_type{}, std::false_type{});
 }
 
 // Tile `id` of tm x tn of them: workgroups are dealt round-robin to the 8
