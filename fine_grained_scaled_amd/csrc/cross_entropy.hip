@@ -246,13 +246,16 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_score_kernel(ScoreArgs p)
 #pragma unroll
             for (int k = 0; k < 16; ++k) top = fmaxf(top, acc[i][j][k]);
         top = fmaxf(top, swap_half(top));
-        const float base = top == -INFINITY ? 0.0f : top;
+        // 2^(z log2 e - base), one multiply-add an exponent; what base's rounding
+        // takes from top log2 e comes back as a factor of the sum
+        const float base = (top == -INFINITY ? 0.0f : top) * LOG2E;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < S::TJ; ++j)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum += __builtin_amdgcn_exp2f((acc[i][j][k] - base) * LOG2E);
+            for (int k = 0; k < 16; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], LOG2E, -base));
         sum += swap_half(sum);
+        if (top != -INFINITY) sum *= __builtin_amdgcn_exp2f(__builtin_fmaf(-top, LOG2E, base));
         if (half == 0) red[wn * S::BM + row] = make_float2(top, sum);
         // the target's value, from the lane that holds it
         int target = -1;
@@ -385,17 +388,27 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_gradient_kernel(ScoreArgs p)
 #pragma unroll
     for (int i = 0; i < S::TI; ++i) {
         const int64_t row = m0 + wm * S::WM + 32 * i + (lane & 31);      // within the padded rows
-        const float lse = p.r.lse[row], b = p.r.dloss[row] / most, a = b + p.r.dlse[row] / most;
-        const int target = p.r.target[row];
+        const float lse = p.r.lse[row] * LOG2E, b = p.r.dloss[row] / most, a = b + p.r.dlse[row] / most;
+        const int64_t in = p.r.target[row] - nw;
 #pragma unroll
         for (int j = 0; j < S::TJ; ++j)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int64_t n = nw + 32 * j + acc_n(k, half);
-                float v = a * __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * LOG2E);
-                if (n == target) v -= b;
-                acc[i][j][k] = row < rows && n < p.V ? v : 0.0f;
-            }
+            for (int k = 0; k < 16; ++k) acc[i][j][k] = a * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], LOG2E, -lse));
+        if (__any(in >= 0 && in < S::WN)) {
+#pragma unroll
+            for (int j = 0; j < S::TJ; ++j)
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (in == 32 * j + acc_n(k, half)) acc[i][j][k] -= b;
+        }
+        // rows and words that only fill the tile up
+        if (m0 + S::BM > rows || nw + S::WN > p.V) {
+#pragma unroll
+            for (int j = 0; j < S::TJ; ++j)
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (row >= rows || nw + 32 * j + acc_n(k, half) >= p.V) acc[i][j][k] = 0.0f;
+        }
     }
     store_tile<S>(smem, [&](int i, int j, int k) { return acc[i][j][k]; },
                   [&](int row, int c) { return p.dz + (m0 + row) * at.ld + (n0 - at.v0) + 8 * c; });
