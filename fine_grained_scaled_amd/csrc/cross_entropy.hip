@@ -37,7 +37,7 @@ namespace {
 using namespace prod;
 
 using Big = Shape<2, 4, 4, 2>;         // 256 x 256, 8 waves of 128 x 64
-using Small = Shape<1, 4, 2, 1, 4>;    // 64 x 128, 4 waves of 64 x 32: up to 64 tokens, bound by the loads of w
+using Small = Shape<2, 4, 2, 1, 4>;    // 128 x 128, 8 waves of 64 x 32, up to 128 tokens: bound by the loads of w
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
@@ -480,6 +480,7 @@ __global__ __launch_bounds__(256) void ce_dx_store_kernel(GradArgs p)
     const int lane = thread & 63, wave = thread >> 6, half = lane >> 5;
     const float4* sums = reinterpret_cast<const float4*>(p.sums) + tile * splits * PER + 2 * pair * S::THREADS + thread;
     float4 a = {}, b = {};
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
         const float4 u = sums[(int64_t)s * PER], v = sums[(int64_t)s * PER + S::THREADS];
         a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
@@ -522,9 +523,12 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_dw_kernel(GradArgs p)
                   });
 }
 
-// Up to 64 tokens the rows of a 256 x 256 tile would be padding for the most
-// part, and its 8 waves would wait for one tile's loads.
-constexpr int64_t SMALL = 64;
+// Up to 128 tokens the pass is bound by reading w, and a 256 x 256 tile's rows
+// would be padding for the most part: 128 x 128 with three stages on their way
+// takes 64 us for 100 tokens, 32000 x 4096 forward (107 with 256 x 256), 207 for
+// 128 tokens, 128000 x 4096 (252).  (64 x 128 in 4 waves: 2% less at 5 tokens,
+// 14 to 30% more from 65 on.)
+constexpr int64_t SMALL = Small::BM;
 // dz of one piece of the vocabulary: 256 MiB, or 8192 words where that is more.
 constexpr int64_t PIECE_VALUES = (int64_t)1 << 27, PIECE_LEAST = 8192;
 // Parts of dx: sums of 1280 tiles at most, where their number is not more
@@ -564,7 +568,7 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool backward, void* workspace)
     p.small = T <= SMALL;
     const int bm = p.small ? Small::BM : Big::BM, bn = p.small ? Small::BN : Big::BN;
     p.Tp = up(std::max<int64_t>(T, 1), 256);
-    // the forward pass of one tile of tokens gains nothing from a list of rows
+    // the forward pass of one tile's tokens gains nothing from a list of rows
     p.list = backward || T > Big::BM;
     if (p.list) {
         p.r.count = at.take<int32_t>(3);

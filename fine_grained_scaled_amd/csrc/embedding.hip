@@ -10,7 +10,7 @@
 // tokens first, stably, so that every sum runs over a contiguous piece of the
 // sorted list in the order of the positions: no atomics, the same bits on every
 // run, and each row of dout is read once.  The sort counts: within chunks of
-// 4096 tokens an entry's place is the number of entries before it (16 waves
+// 2048 tokens an entry's place is the number of entries before it (16 waves
 // compare 64 entries with the whole chunk from LDS), and a chunk's entries find
 // their places among the other chunks by binary search.  Two launches for any
 // number of tokens; the first also clears dw, which takes longer than the sort.
@@ -30,8 +30,10 @@ namespace fgs {
 
 namespace {
 
-constexpr int CHUNK = 4096;            // tokens sorted at once
+constexpr int CHUNK = 2048;            // tokens sorted at once
 constexpr int TABLE = 64;              // entries a workgroup places
+constexpr int SEARCHES = 4;            // chunks that a wave searches at once
+constexpr int MERGERS = 8;             // waves that search for the same entries
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -123,6 +125,7 @@ struct SortArgs {
     uint4* clear;                      // dw, where the call clears it
     int64_t clear_vecs;
     int sorters;                       // workgroups that sort; the others clear
+    int* spanning;                     // a counter to clear
 };
 
 __global__ __launch_bounds__(1024) void embedding_sort_kernel(SortArgs p)
@@ -135,6 +138,7 @@ __global__ __launch_bounds__(1024) void embedding_sort_kernel(SortArgs p)
             p.clear[i] = make_uint4(0, 0, 0, 0);
         return;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int first = blockIdx.x * TABLE, base = first & ~(CHUNK - 1);
     for (int i = threadIdx.x; i < CHUNK; i += 1024) {
@@ -151,20 +155,29 @@ __global__ __launch_bounds__(1024) void embedding_sort_kernel(SortArgs p)
     const int n = min(CHUNK, p.T - base), per = CHUNK / 16;
     const int lo = wave * per, hi = min(lo + per, n);
     const int4* keys = reinterpret_cast<const int4*>(s_key);
+    const int block = first - base;                // the entries placed here
     int rank = 0;
-    for (int k = lo; k < hi; k += 4) {             // entries past n hold the largest key and count for none
+    int k = lo;
+    // equal keys in front of an entry come before it, those behind it do not;
+    // what lies past the tokens holds the largest key and counts for none
+    for (; k < min(hi, block); k += 4) {
         const int4 q = keys[k / 4];
-        rank += q.x < key + (k < mine);            // an equal key in front of this one counts
-        rank += q.y < key + (k + 1 < mine);
-        rank += q.z < key + (k + 2 < mine);
-        rank += q.w < key + (k + 3 < mine);
+        rank += (q.x <= key) + (q.y <= key) + (q.z <= key) + (q.w <= key);
+    }
+    for (; k < min(hi, block + TABLE); k += 4) {
+        const int4 q = keys[k / 4];
+        rank += (q.x < key + (k < mine)) + (q.y < key + (k + 1 < mine)) + (q.z < key + (k + 2 < mine)) + (q.w < key + (k + 3 < mine));
+    }
+    for (; k < hi; k += 4) {
+        const int4 q = keys[k / 4];
+        rank += (q.x < key) + (q.y < key) + (q.z < key) + (q.w < key);
     }
     atomicAdd(&s_rank[lane], rank);
     __syncthreads();
     if (wave == 0 && first + lane < p.T) p.sorted[base + s_rank[lane]] = make_int2(key, first + lane);
 }
 
-__global__ __launch_bounds__(1024) void embedding_merge_kernel(SortArgs p)
+__global__ __launch_bounds__(64 * MERGERS) void embedding_merge_kernel(SortArgs p)
 {
     __shared__ int s_rank[TABLE];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -175,14 +188,27 @@ __global__ __launch_bounds__(1024) void embedding_merge_kernel(SortArgs p)
     const int2 entry = p.sorted[e];
     const int chunks = (p.T + CHUNK - 1) / CHUNK;
     int rank = 0;
-    for (int c = wave; c < chunks; c += 16) {
-        if (c == chunk) continue;
-        const int2* at = p.sorted + c * CHUNK;
-        const int n = min(CHUNK, p.T - c * CHUNK), below = entry.x + (c < chunk);      // keys below this one come first
-        int found = 0;
-        for (int step = CHUNK; step > 0; step >>= 1)
-            if (found + step <= n && at[found + step - 1].x < below) found += step;
-        rank += found;
+    for (int c0 = wave; c0 < chunks; c0 += MERGERS * SEARCHES) {
+        // several chunks at a time: a search is a chain of loads
+        const int2* at[SEARCHES];
+        int n[SEARCHES], below[SEARCHES], found[SEARCHES] = {};
+#pragma unroll
+        for (int k = 0; k < SEARCHES; ++k) {
+            const int c = c0 + MERGERS * k;
+            at[k] = p.sorted + min(c, chunks - 1) * CHUNK;
+            n[k] = c < chunks ? min(CHUNK, p.T - c * CHUNK) : 0;
+            below[k] = entry.x + (c < chunk);          // keys below this one come first
+        }
+#pragma unroll
+        for (int step = CHUNK; step > 0; step >>= 1) {
+            int key[SEARCHES];
+#pragma unroll
+            for (int k = 0; k < SEARCHES; ++k) key[k] = at[k][max(min(found[k] + step, n[k]) - 1, 0)].x;
+#pragma unroll
+            for (int k = 0; k < SEARCHES; ++k) found[k] += found[k] + step <= n[k] && key[k] < below[k] ? step : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < SEARCHES; ++k) rank += c0 + MERGERS * k != chunk ? found[k] : 0;
     }
     atomicAdd(&s_rank[lane], rank);
     __syncthreads();
@@ -194,126 +220,156 @@ __global__ __launch_bounds__(1024) void embedding_merge_kernel(SortArgs p)
 // ------------------------------------------------------------------------
 struct SumArgs {
     const int2* list;                  // T entries
-    int T, V, vecs, piece, pieces, shift;
+    int T, V, W, piece, pieces, shift;
     const void* dout;
     int64_t ldd;
     void* dw;
     float scale;
     int add;                           // to what dw holds
-    float* parts;                      // [pieces][2][8 vecs]: a piece's first and its last sum
+    float* parts;                      // [pieces][2][W]: a piece's first and its last sum
+    int* spanning;                     // how many sums span pieces, and the pieces in which they begin (in any order)
 };
 
-template <bool WB>
-__device__ __forceinline__ void write_sum(const SumArgs& p, int key, int vec, const float sum[8])
+// dw's row `key`, columns col .. col + N - 1
+template <bool WB, int N>
+__device__ __forceinline__ void write_sum(const SumArgs& p, int key, int col, const float* sum)
 {
-    char* row = const_cast<char*>(row_of<WB>(p.dw, key, 8 * (int64_t)p.vecs));
-    float f[8] = {};
-    if (p.add) {
-        Eight<WB> old;
-        old.load(row, vec);
-        old.get(f);
-    }
+    if constexpr (WB) {
+        uint16_t* at = static_cast<uint16_t*>(p.dw) + (int64_t)key * p.W + col;
+        uint32_t w[N / 2] = {};
+        if (p.add) {
+            if constexpr (N == 8) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at);
+            else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
+        }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] += p.scale * sum[k];
-    Eight<WB>::store(row, vec, f);
+        for (int i = 0; i < N / 2; ++i) {
+            const bf16x2 v = {(__bf16)(bf16_lo(w[i]) + p.scale * sum[2 * i]), (__bf16)(bf16_hi(w[i]) + p.scale * sum[2 * i + 1])};
+            w[i] = __builtin_bit_cast(uint32_t, v);
+        }
+        if constexpr (N == 8) *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(w);
+        else *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(w);
+    } else {
+        float4* at = reinterpret_cast<float4*>(static_cast<float*>(p.dw) + (int64_t)key * p.W + col);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            float4 v = p.add ? at[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v.x += p.scale * sum[4 * i], v.y += p.scale * sum[4 * i + 1];
+            v.z += p.scale * sum[4 * i + 2], v.w += p.scale * sum[4 * i + 3];
+            at[i] = v;
+        }
+    }
 }
 
-template <bool DB, bool WB>
+// 16 bytes of a row a thread: 8 BF16 or 4 FP32 columns.  WAVES: a piece takes
+// whole waves, which then read the list once for all their lanes.
+template <bool DB, bool WB, bool WAVES>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs p)
 {
-    constexpr int AHEAD = 8;
-    const int piece = ((int)blockIdx.x << (8 - p.shift)) + (threadIdx.x >> p.shift);
-    const int vec = (int)(blockIdx.y << p.shift) + (threadIdx.x & ((1 << p.shift) - 1));
-    if (piece >= p.pieces || vec >= p.vecs) return;
+    constexpr int N = DB ? 8 : 4, AHEAD = 16;
+    int piece = ((int)blockIdx.x << (8 - p.shift)) + (threadIdx.x >> p.shift);
+    if (WAVES) piece = __builtin_amdgcn_readfirstlane(piece);
+    const int wanted = N * ((int)(blockIdx.y << p.shift) + (threadIdx.x & ((1 << p.shift) - 1)));
+    if (piece >= p.pieces) return;
+    const int col = min(wanted, p.W - N);          // lanes past the row stay to hand out the list, and write nothing
     const int begin = piece * p.piece, end = min(begin + p.piece, p.T);
     const int before = begin > 0 ? p.list[begin - 1].x : -1, after = end < p.T ? p.list[end].x : -1;
-    float* part = p.parts + ((int64_t)piece * 2 * p.vecs + vec) * 8;
-    float sum[8] = {};
+    float* part = p.parts + (int64_t)piece * 2 * p.W + col;
+    float sum[N] = {};
     int key = p.list[begin].x;
     bool first = true;                 // the run in hand began in front of the piece, or at its first entry
     // the run in hand is complete, or the piece ends
     auto flush = [&](bool last) {
-        if (key >= p.V) return;
+        if (key >= p.V || wanted >= p.W) return;
         const bool cut_before = first && before == key, cut_after = last && after == key;
-        if (!cut_before && !cut_after) return write_sum<WB>(p, key, vec, sum);
+        if (!cut_before && !cut_after) return write_sum<WB, N>(p, key, col, sum);
+        if (!cut_before && col == 0) p.spanning[1 + atomicAdd(p.spanning, 1)] = piece;
         // a whole piece of one token counts as a first sum
-        Eight<false>::store(part + (cut_before ? 0 : 8 * (int64_t)p.vecs), 0, sum);
+        float4* to = reinterpret_cast<float4*>(part + (cut_before ? 0 : p.W));
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) to[i] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
     };
     for (int i = begin; i < end; i += AHEAD) {
         int2 e[AHEAD];
-        Eight<DB> row[AHEAD];
+        uint4 row[AHEAD];
+        if constexpr (WAVES) {         // a lane's entry each, handed to all
+            const int2 mine = p.list[min(i + (int)(threadIdx.x & (AHEAD - 1)), end - 1)];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) e[k] = p.list[min(i + k, end - 1)];
+            for (int k = 0; k < AHEAD; ++k)
+                e[k] = make_int2(__builtin_amdgcn_readlane(mine.x, k), __builtin_amdgcn_readlane(mine.y, k));
+        } else {
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) row[k].load(row_of<DB>(p.dout, e[k].y, p.ldd), vec);
+            for (int k = 0; k < AHEAD; ++k) e[k] = p.list[min(i + k, end - 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            row[k] = *reinterpret_cast<const uint4*>(row_of<DB>(p.dout, e[k].y, p.ldd) + (DB ? 2 : 4) * (int64_t)col);
+        // all loads are on their way before the first is used: the compiler would
+        // move each behind the branches in front of its use
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) asm volatile("" : "+v"(row[k].x), "+v"(row[k].y), "+v"(row[k].z), "+v"(row[k].w));
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            if (i + k >= end) break;
-            if (e[k].x != key) {
+            const bool there = i + k < end;
+            if (there && e[k].x != key) {
                 flush(false);
                 key = e[k].x;
                 first = false;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+                for (int j = 0; j < N; ++j) sum[j] = 0.0f;
             }
-            float f[8];
-            row[k].get(f);
+            const uint32_t w[4] = {row[k].x, row[k].y, row[k].z, row[k].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += f[j];
+            for (int j = 0; j < N; ++j) {
+                const float v = DB ? j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]) : as_f32(w[j]);
+                sum[j] = there ? sum[j] + v : sum[j];
+            }
         }
     }
     flush(true);
 }
 
-// The sums that span pieces: the piece in which one begins finds the last that
-// it reaches and adds the parts, 16 at a time over the workgroup's rows.
+// The sums that span pieces: from the piece in which one begins to the last that
+// it reaches, the parts are added in the order of their numbers' residues by 16
+// (a wave each, four columns a lane).
 template <bool WB>
 __global__ __launch_bounds__(1024) void embedding_join_kernel(SumArgs p)
 {
-    __shared__ float s_sum[16][64][9];
+    __shared__ float4 s_sum[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int piece = blockIdx.x;                          // there is one behind it
-    const int begin = piece * p.piece, next = begin + p.piece;
-    const int key = p.list[next - 1].x;
-    if (key >= p.V || p.list[next].x != key) return;
-    const bool whole = p.list[begin].x == key;
-    if (whole && begin > 0 && p.list[begin - 1].x == key) return;      // began earlier
-    int last = piece;
-    for (;;) {
-        const int c = last + 1 + lane;
-        const uint64_t same = __ballot(c < p.pieces && p.list[(int64_t)c * p.piece].x == key);
-        const int run = same == ~0ull ? 64 : __builtin_ctzll(~same);
-        last += run;
-        if (run < 64) break;
-    }
-    const int vec = (int)blockIdx.y * 64 + lane;
-    const int64_t row = 8 * (int64_t)p.vecs;
-    float sum[8] = {};
-    if (vec < p.vecs) {
-        for (int c = piece + wave; c <= last; c += 16) {
-            Eight<false> e;
-            e.load(p.parts + 2 * row * c + (c == piece ? row : 0), vec);
-            float f[8];
-            e.get(f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += f[k];
+    const int count = p.spanning[0], col = 4 * ((int)blockIdx.y * 64 + lane);
+    for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        const int piece = p.spanning[1 + i];
+        const int key = p.list[(piece + 1) * p.piece].x;
+        // the pieces that begin with the key: of the next 64, and where these all do, of 1024 at a time
+        auto begins = [&](int64_t c) { return c < p.pieces && p.list[c * p.piece].x == key; };
+        const uint64_t same = __ballot(begins(piece + 2 + lane));
+        int last = piece + 1 + (same == ~0ull ? 64 : __builtin_ctzll(~same));
+        for (int more = last == piece + 65 ? 1024 : 0; more == 1024; last += more) more = __syncthreads_count(begins(last + 1 + (int)threadIdx.x));
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (col < p.W) {
+#pragma unroll 8
+            for (int c = piece + wave; c <= last; c += 16) {
+                const float4 v = *reinterpret_cast<const float4*>(p.parts + (2 * (int64_t)c + (c == piece)) * p.W + col);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
         }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s_sum[wave][lane][k] = sum[k];
-    __syncthreads();
-    if (wave == 0 && vec < p.vecs) {
-        const int waves = min(16, last - piece + 1);
-        for (int w = 1; w < waves; ++w)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += s_sum[w][lane][k];
-        write_sum<WB>(p, key, vec, sum);
+        s_sum[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && col < p.W) {
+            const int waves = min(16, last - piece + 1);
+            for (int w = 1; w < waves; ++w) {
+                const float4 v = s_sum[w][lane];
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+            write_sum<WB, 4>(p, key, col, &sum.x);
+        }
+        __syncthreads();
     }
 }
 
 struct Plan {
-    int vecs, shift, columns, piece, pieces;
-    int64_t sorted, merged, parts, bytes;      // offsets into the workspace
+    int shift, columns, piece, pieces;
+    int64_t sorted, merged, spanning, parts, bytes;      // offsets into the workspace
 };
 
 // threads a row: a power of two, 256 at most
@@ -324,13 +380,13 @@ int row_shift(int64_t vecs)
     return s;
 }
 
-Plan make_plan(int64_t T, int64_t W)
+Plan make_plan(int64_t T, int64_t W, bool bf16)
 {
     Plan p;
-    p.vecs = (int)(W / 8);
-    p.shift = row_shift(p.vecs);
-    p.columns = (p.vecs + (1 << p.shift) - 1) >> p.shift;
-    // pieces long enough for a thread's loads to overlap, short enough for about 1024 workgroups
+    const int64_t vecs = W / (bf16 ? 8 : 4);
+    p.shift = row_shift(vecs);
+    p.columns = (int)((vecs + (1 << p.shift) - 1) >> p.shift);
+    // pieces as long as a thread's loads that overlap, longer where there are more than about 1024 workgroups
     const int64_t work = (T * p.columns) >> (8 - p.shift);
     p.piece = 16;
     while (p.piece < 256 && work / p.piece > 1024) p.piece *= 2;
@@ -338,14 +394,18 @@ Plan make_plan(int64_t T, int64_t W)
     const auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
     p.sorted = 0;
     p.merged = up(8 * T);
-    p.parts = p.merged + (T > CHUNK ? up(8 * T) : 0);
+    p.spanning = p.merged + (T > CHUNK ? up(8 * T) : 0);
+    p.parts = p.spanning + up(4 * (1 + p.pieces));
     p.bytes = p.parts + (p.pieces > 1 ? 8 * p.pieces * W : 0);
     return p;
 }
 
 } // namespace
 
-size_t embedding_workspace_bytes(int64_t T, int64_t W) { return (size_t)make_plan(T, W).bytes; }
+size_t embedding_workspace_bytes(int64_t T, int64_t W)
+{
+    return (size_t)std::max(make_plan(T, W, false).bytes, make_plan(T, W, true).bytes);
+}
 
 hipError_t launch_embedding_fwd(const EmbeddingArgs& a, hipStream_t stream)
 {
@@ -359,12 +419,13 @@ hipError_t launch_embedding_fwd(const EmbeddingArgs& a, hipStream_t stream)
 
 hipError_t launch_embedding_bwd(const EmbeddingArgs& a, hipStream_t stream)
 {
-    const Plan p = make_plan(a.T, a.W);
+    const Plan p = make_plan(a.T, a.W, a.bf16 != 0);
     char* ws = static_cast<char*>(a.workspace);
     SortArgs s{};
     s.tokens = a.tokens, s.wide = a.wide, s.T = (int)a.T, s.V = (int)a.V;
     s.sorted = reinterpret_cast<int2*>(ws + p.sorted), s.merged = reinterpret_cast<int2*>(ws + p.merged);
     s.sorters = (int)((a.T + TABLE - 1) / TABLE);
+    s.spanning = reinterpret_cast<int*>(ws + p.spanning);
     int64_t clearers = 0;
     if (!a.add) {
         s.clear = static_cast<uint4*>(a.dweight);
@@ -375,19 +436,25 @@ hipError_t launch_embedding_bwd(const EmbeddingArgs& a, hipStream_t stream)
     embedding_sort_kernel<<<(uint32_t)(s.sorters + clearers), 1024, 0, stream>>>(s);
     if (a.T == 0) return hipGetLastError();
     const bool chunks = a.T > CHUNK;
-    if (chunks) embedding_merge_kernel<<<(uint32_t)s.sorters, 1024, 0, stream>>>(s);
+    if (chunks) embedding_merge_kernel<<<(uint32_t)s.sorters, 64 * MERGERS, 0, stream>>>(s);
     SumArgs m{};
     m.list = chunks ? s.merged : s.sorted;
-    m.T = s.T, m.V = s.V, m.vecs = p.vecs, m.piece = p.piece, m.pieces = p.pieces, m.shift = p.shift;
+    m.T = s.T, m.V = s.V, m.W = (int)a.W, m.piece = p.piece, m.pieces = p.pieces, m.shift = p.shift;
     m.dout = a.dout, m.ldd = a.ldd, m.dw = a.dweight, m.scale = a.scale, m.add = a.add;
-    m.parts = reinterpret_cast<float*>(ws + p.parts);
+    m.parts = reinterpret_cast<float*>(ws + p.parts), m.spanning = s.spanning;
     const dim3 grid((uint32_t)((p.pieces + (256 >> p.shift) - 1) / (256 >> p.shift)), (uint32_t)p.columns);
-    auto sum = a.bf16 ? a.weight_bf16 ? embedding_sum_kernel<true, true> : embedding_sum_kernel<true, false>
-                      : a.weight_bf16 ? embedding_sum_kernel<false, true> : embedding_sum_kernel<false, false>;
+    void (*sum)(SumArgs);
+    if (p.shift >= 6)
+        sum = a.bf16 ? a.weight_bf16 ? embedding_sum_kernel<true, true, true> : embedding_sum_kernel<true, false, true>
+                     : a.weight_bf16 ? embedding_sum_kernel<false, true, true> : embedding_sum_kernel<false, false, true>;
+    else
+        sum = a.bf16 ? a.weight_bf16 ? embedding_sum_kernel<true, true, false> : embedding_sum_kernel<true, false, false>
+                     : a.weight_bf16 ? embedding_sum_kernel<false, true, false> : embedding_sum_kernel<false, false, false>;
     sum<<<grid, 256, 0, stream>>>(m);
     if (p.pieces > 1) {
         auto join = a.weight_bf16 ? embedding_join_kernel<true> : embedding_join_kernel<false>;
-        join<<<dim3((uint32_t)(p.pieces - 1), (uint32_t)((p.vecs + 63) / 64)), 1024, 0, stream>>>(m);
+        const int64_t columns = (a.W + 255) / 256;
+        join<<<dim3((uint32_t)std::min<int64_t>(p.pieces - 1, std::max<int64_t>(8, 1024 / columns)), (uint32_t)columns), 1024, 0, stream>>>(m);
     }
     return hipGetLastError();
 }
