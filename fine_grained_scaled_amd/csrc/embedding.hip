@@ -33,6 +33,7 @@ namespace {
 constexpr int CHUNK = 2048;            // tokens sorted at once
 constexpr int TABLE = 64;              // entries a workgroup places
 constexpr int SEARCHES = 4;            // chunks that a wave searches at once
+constexpr int JOINERS = 8;             // waves that add one sum's parts
 constexpr int MERGERS = 8;             // waves that search for the same entries
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -329,26 +330,26 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs p)
 }
 
 // The sums that span pieces: from the piece in which one begins to the last that
-// it reaches, the parts are added in the order of their numbers' residues by 16
+// it reaches, the parts are added in the order of their numbers' residues by 8
 // (a wave each, four columns a lane).
 template <bool WB>
-__global__ __launch_bounds__(1024) void embedding_join_kernel(SumArgs p)
+__global__ __launch_bounds__(64 * JOINERS) void embedding_join_kernel(SumArgs p)
 {
-    __shared__ float4 s_sum[16][64];
+    __shared__ float4 s_sum[JOINERS][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int count = p.spanning[0], col = 4 * ((int)blockIdx.y * 64 + lane);
     for (int i = blockIdx.x; i < count; i += gridDim.x) {
         const int piece = p.spanning[1 + i];
         const int key = p.list[(piece + 1) * p.piece].x;
-        // the pieces that begin with the key: of the next 64, and where these all do, of 1024 at a time
+        // the pieces that begin with the key: of the next 64, and where these all do, of the workgroup's threads at a time
         auto begins = [&](int64_t c) { return c < p.pieces && p.list[c * p.piece].x == key; };
         const uint64_t same = __ballot(begins(piece + 2 + lane));
         int last = piece + 1 + (same == ~0ull ? 64 : __builtin_ctzll(~same));
-        for (int more = last == piece + 65 ? 1024 : 0; more == 1024; last += more) more = __syncthreads_count(begins(last + 1 + (int)threadIdx.x));
+        for (int more = last == piece + 65 ? 64 * JOINERS : 0; more == 64 * JOINERS; last += more) more = __syncthreads_count(begins(last + 1 + (int)threadIdx.x));
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (col < p.W) {
-#pragma unroll 8
-            for (int c = piece + wave; c <= last; c += 16) {
+#pragma unroll 16
+            for (int c = piece + wave; c <= last; c += JOINERS) {
                 const float4 v = *reinterpret_cast<const float4*>(p.parts + (2 * (int64_t)c + (c == piece)) * p.W + col);
                 sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
             }
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(1024) void embedding_join_kernel(SumArgs p)
         s_sum[wave][lane] = sum;
         __syncthreads();
         if (wave == 0 && col < p.W) {
-            const int waves = min(16, last - piece + 1);
+            const int waves = min(JOINERS, last - piece + 1);
             for (int w = 1; w < waves; ++w) {
                 const float4 v = s_sum[w][lane];
                 sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
@@ -454,7 +455,7 @@ hipError_t launch_embedding_bwd(const EmbeddingArgs& a, hipStream_t stream)
     if (p.pieces > 1) {
         auto join = a.weight_bf16 ? embedding_join_kernel<true> : embedding_join_kernel<false>;
         const int64_t columns = (a.W + 255) / 256;
-        join<<<dim3((uint32_t)std::min<int64_t>(p.pieces - 1, std::max<int64_t>(8, 1024 / columns)), (uint32_t)columns), 1024, 0, stream>>>(m);
+        join<<<dim3((uint32_t)std::min<int64_t>(p.pieces - 1, std::max<int64_t>(8, 2048 / columns)), (uint32_t)columns), 64 * JOINERS, 0, stream>>>(m);
     }
     return hipGetLastError();
 }

@@ -739,8 +739,9 @@ static int check_head(int64_t T, int64_t V, int64_t K, int index_dtype)
         return fail(FGS_ERR_INVALID_ARG, "index_dtype %d is not FGS_INDEX_I32 or FGS_INDEX_I64", index_dtype);
     if (K % 64 || K > 65536) return fail(FGS_ERR_UNSUPPORTED, "width must be a multiple of 64, at most 65536 (got %lld)", (long long)K);
     // a launch has fewer than 2^32 threads
-    if (T > (1 << 23) || V > (1 << 24) || ((T + 255) / 256) * ((V + 127) / 128) > (1 << 22))
-        return fail(FGS_ERR_UNSUPPORTED, "tokens (%lld) or vocab (%lld) too large", (long long)T, (long long)V);
+    if (T > (1 << 23) || V > (1 << 24) || ((T + 255) / 256) * ((V + 127) / 128) > (1 << 22) || T * K > (int64_t)1 << 34 ||
+        V * K > (int64_t)1 << 38)
+        return fail(FGS_ERR_UNSUPPORTED, "tokens (%lld), vocab (%lld) or width (%lld) too large", (long long)T, (long long)V, (long long)K);
     return FGS_OK;
 }
 

@@ -676,7 +676,8 @@ enum { FGS_INDEX_I32 = 0, FGS_INDEX_I64 = 1 };
  * x        BF16 [tokens x width], row stride ldx; w: BF16 [vocab x width], row
  *          stride ldw.  width a multiple of 64, at most 65536; strides multiples of 8
  *          (a single row's may be anything); pointers 16-byte aligned.  At most
- *          2^23 tokens and 2^22 tiles of 256 tokens and 128 words.
+ *          2^23 tokens, 2^24 words, 2^22 tiles of 256 tokens and 128 words, 2^34
+ *          values of x and 2^38 of w.
  * targets  DEVICE int32 or int64 (index_dtype FGS_INDEX_*) [tokens].
  * loss, lse  FP32 [tokens].
  * Products are exact and summed in FP32, as are exponents.  A row whose
@@ -757,7 +758,7 @@ size_t fgs_embedding_workspace_bytes(int64_t count, int64_t width);
  *          tiles first: where inter is a multiple of 128, what
  *          fgs_quantize_blockwise gives for gate_up.
  * inter and strides multiples of 8 (a single row's stride may be anything);
- * pointers 16-byte aligned.
+ * pointers 16-byte aligned; at most 1048560 rows.
  */
 int fgs_swiglu_fwd(const void *gate_up, int64_t rows, int64_t inter, int64_t ld, void *h, uint8_t *q, float *scales,
                    void *stream);

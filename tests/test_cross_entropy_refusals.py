@@ -46,7 +46,8 @@ def test_backward_invalid(how):
 
 
 UNSUPPORTED = [dict(K=96), dict(K=65600, ldx=65600, ldw=65600), dict(ldx=132), dict(ldw=130), dict(x=FAKE + 8), dict(w=FAKE + 2),
-               dict(T=(1 << 23) + 1), dict(V=(1 << 24) + 1), dict(T=1 << 22, V=1 << 20)]
+               dict(T=(1 << 23) + 1), dict(V=(1 << 24) + 1), dict(T=1 << 22, V=1 << 20),
+               dict(T=1 << 20, K=32768, ldx=32768, ldw=32768), dict(V=1 << 23, K=65536, ldx=65536, ldw=65536)]
 
 
 @pytest.mark.parametrize("how", UNSUPPORTED, ids=str)
