@@ -56,8 +56,11 @@ class Block(torch.nn.Module):
         q, k, v = self.qkv(n).view(tokens, -1, self.dim).split(self.split, 1)    # views: nothing is copied
         y = self.out(fgs.attention(q, k, v, cu_seqlens).view(tokens, width))
         x, n = self.after_attention(y, x)
-        a, b = self.up(n).chunk(2, 1)
-        return self.after_mlp(self.down(torch.nn.functional.silu(a) * b), x)
+        return self.after_mlp(self.down(self.activate(self.up(n))), x)
+
+    def activate(self, gate_up):
+        a, b = gate_up.chunk(2, 1)
+        return torch.nn.functional.silu(a) * b
 
 
 def train(steps=10, tokens=1024, width=512, heads=8, kv_heads=2, hidden=1024, layers=2, max_norm=1.0, lr=2e-3, seed=0,
