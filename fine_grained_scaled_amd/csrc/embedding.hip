@@ -12,14 +12,15 @@
 // run, and each row of dout is read once.  The sort counts: within chunks of
 // 2048 tokens an entry's place is the number of entries before it (16 waves
 // compare 64 entries with the whole chunk from LDS), and a chunk's entries find
-// their places among the other chunks by binary search.  Two launches for any
-// number of tokens; the first also clears dw, which takes longer than the sort.
+// their places among the other chunks by binary search: two launches for any
+// number of tokens.
 //
 // The sorted list is cut into pieces of equal length whatever the tokens are, so
 // that one token in most positions (padding) is summed by as many workgroups as
 // any other input.  A sum that lies in one piece is written at once; the parts
 // of one that spans pieces go to the workspace, and a last kernel adds them in
-// the pieces' order.
+// a fixed order.  The rows that no token is get their zeros from workgroups of
+// their own in the launch that sums, so each row of dw is written once.
 #include <algorithm>
 #include <climits>
 
@@ -33,6 +34,7 @@ namespace {
 constexpr int CHUNK = 2048;            // tokens sorted at once
 constexpr int TABLE = 64;              // entries a workgroup places
 constexpr int SEARCHES = 4;            // chunks that a wave searches at once
+constexpr int ZERO_ROWS = 64;          // rows of dw that a workgroup looks up and clears
 constexpr int JOINERS = 8;             // waves that add one sum's parts
 constexpr int MERGERS = 8;             // waves that search for the same entries
 
@@ -123,9 +125,6 @@ struct SortArgs {
     int wide;
     int T, V;
     int2 *sorted, *merged;             // (key, position): by chunk, and of all
-    uint4* clear;                      // dw, where the call clears it
-    int64_t clear_vecs;
-    int sorters;                       // workgroups that sort; the others clear
     int* spanning;                     // a counter to clear
 };
 
@@ -133,12 +132,6 @@ __global__ __launch_bounds__(1024) void embedding_sort_kernel(SortArgs p)
 {
     __shared__ int s_key[CHUNK];
     __shared__ int s_rank[TABLE];
-    if ((int)blockIdx.x >= p.sorters) {
-        const int64_t step = (int64_t)(gridDim.x - p.sorters) * 1024;
-        for (int64_t i = (int64_t)(blockIdx.x - p.sorters) * 1024 + threadIdx.x; i < p.clear_vecs; i += step)
-            p.clear[i] = make_uint4(0, 0, 0, 0);
-        return;
-    }
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int first = blockIdx.x * TABLE, base = first & ~(CHUNK - 1);
@@ -229,7 +222,36 @@ struct SumArgs {
     int add;                           // to what dw holds
     float* parts;                      // [pieces][2][W]: a piece's first and its last sum
     int* spanning;                     // how many sums span pieces, and the pieces in which they begin (in any order)
+    int summers, columns;              // workgroups that sum, in front of those that write zeros; blocks along a row
 };
+
+// Zeros to those of rows first .. first + ZERO_ROWS - 1 of dw that no token is:
+// a thread looks a row up in the sorted list.
+template <bool WB>
+__device__ __forceinline__ void write_zeros(const SumArgs& p, int64_t first)
+{
+    __shared__ uint8_t s_idle[ZERO_ROWS];
+    const int rows = (int)min((int64_t)ZERO_ROWS, p.V - first);
+    if ((int)threadIdx.x < rows) {
+        const int key = (int)first + threadIdx.x;
+        int found = 0;                 // entries below the key
+        for (int step = 1 << (31 - __builtin_clz(p.T | 1)); step > 0; step >>= 1)
+            if (found + step <= p.T && p.list[found + step - 1].x < key) found += step;
+        s_idle[threadIdx.x] = found == p.T || p.list[found].x != key;
+    }
+    __syncthreads();
+    const int vecs = p.W * (WB ? 2 : 4) / 16;
+    uint4* base = static_cast<uint4*>(p.dw) + first * vecs;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (vecs >= 256) {
+        for (int r = 0; r < rows; ++r)
+            if (s_idle[r])
+                for (int i = threadIdx.x; i < vecs; i += 256) base[(int64_t)r * vecs + i] = zero;
+    } else {
+        for (int i = threadIdx.x; i < rows * vecs; i += 256)
+            if (s_idle[i / vecs]) base[i] = zero;
+    }
+}
 
 // dw's row `key`, columns col .. col + N - 1
 template <bool WB, int N>
@@ -267,9 +289,11 @@ template <bool DB, bool WB, bool WAVES>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs p)
 {
     constexpr int N = DB ? 8 : 4, AHEAD = 16;
-    int piece = ((int)blockIdx.x << (8 - p.shift)) + (threadIdx.x >> p.shift);
+    if ((int)blockIdx.x >= p.summers) return write_zeros<WB>(p, (int64_t)((int)blockIdx.x - p.summers) * ZERO_ROWS);
+    const int block = blockIdx.x, across = block % p.columns;
+    int piece = (block / p.columns << (8 - p.shift)) + (threadIdx.x >> p.shift);
     if (WAVES) piece = __builtin_amdgcn_readfirstlane(piece);
-    const int wanted = N * ((int)(blockIdx.y << p.shift) + (threadIdx.x & ((1 << p.shift) - 1)));
+    const int wanted = N * ((across << p.shift) + (threadIdx.x & ((1 << p.shift) - 1)));
     if (piece >= p.pieces) return;
     const int col = min(wanted, p.W - N);          // lanes past the row stay to hand out the list, and write nothing
     const int begin = piece * p.piece, end = min(begin + p.piece, p.T);
@@ -425,25 +449,20 @@ hipError_t launch_embedding_bwd(const EmbeddingArgs& a, hipStream_t stream)
     SortArgs s{};
     s.tokens = a.tokens, s.wide = a.wide, s.T = (int)a.T, s.V = (int)a.V;
     s.sorted = reinterpret_cast<int2*>(ws + p.sorted), s.merged = reinterpret_cast<int2*>(ws + p.merged);
-    s.sorters = (int)((a.T + TABLE - 1) / TABLE);
     s.spanning = reinterpret_cast<int*>(ws + p.spanning);
-    int64_t clearers = 0;
-    if (!a.add) {
-        s.clear = static_cast<uint4*>(a.dweight);
-        s.clear_vecs = a.V * a.W * (a.weight_bf16 ? 2 : 4) / 16;
-        clearers = std::min<int64_t>(2048, (s.clear_vecs + 1023) / 1024);
-    }
-    if (s.sorters + clearers == 0) return hipSuccess;
-    embedding_sort_kernel<<<(uint32_t)(s.sorters + clearers), 1024, 0, stream>>>(s);
-    if (a.T == 0) return hipGetLastError();
+    const uint32_t tables = (uint32_t)((a.T + TABLE - 1) / TABLE);
     const bool chunks = a.T > CHUNK;
-    if (chunks) embedding_merge_kernel<<<(uint32_t)s.sorters, 64 * MERGERS, 0, stream>>>(s);
+    if (tables) embedding_sort_kernel<<<tables, 1024, 0, stream>>>(s);
+    if (chunks) embedding_merge_kernel<<<tables, 64 * MERGERS, 0, stream>>>(s);
     SumArgs m{};
     m.list = chunks ? s.merged : s.sorted;
     m.T = s.T, m.V = s.V, m.W = (int)a.W, m.piece = p.piece, m.pieces = p.pieces, m.shift = p.shift;
     m.dout = a.dout, m.ldd = a.ldd, m.dw = a.dweight, m.scale = a.scale, m.add = a.add;
     m.parts = reinterpret_cast<float*>(ws + p.parts), m.spanning = s.spanning;
-    const dim3 grid((uint32_t)((p.pieces + (256 >> p.shift) - 1) / (256 >> p.shift)), (uint32_t)p.columns);
+    m.columns = p.columns;
+    m.summers = (p.pieces + (256 >> p.shift) - 1) / (256 >> p.shift) * p.columns;
+    const int64_t grid = m.summers + (a.add ? 0 : (a.V + ZERO_ROWS - 1) / ZERO_ROWS);
+    if (grid == 0) return hipSuccess;
     void (*sum)(SumArgs);
     if (p.shift >= 6)
         sum = a.bf16 ? a.weight_bf16 ? embedding_sum_kernel<true, true, true> : embedding_sum_kernel<true, false, true>
@@ -451,7 +470,7 @@ hipError_t launch_embedding_bwd(const EmbeddingArgs& a, hipStream_t stream)
     else
         sum = a.bf16 ? a.weight_bf16 ? embedding_sum_kernel<true, true, false> : embedding_sum_kernel<true, false, false>
                      : a.weight_bf16 ? embedding_sum_kernel<false, true, false> : embedding_sum_kernel<false, false, false>;
-    sum<<<grid, 256, 0, stream>>>(m);
+    sum<<<(uint32_t)grid, 256, 0, stream>>>(m);
     if (p.pieces > 1) {
         auto join = a.weight_bf16 ? embedding_join_kernel<true> : embedding_join_kernel<false>;
         const int64_t columns = (a.W + 255) / 256;

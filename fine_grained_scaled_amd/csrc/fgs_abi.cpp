@@ -814,7 +814,7 @@ static int check_embedding(const void* tokens, int index_dtype, int64_t count, i
         if (d != FGS_OUT_FP32 && d != FGS_OUT_BF16) return fail(FGS_ERR_INVALID_ARG, "dtype %d is not FGS_OUT_FP32 or FGS_OUT_BF16", d);
     if (!(scale - scale == 0.0f)) return fail(FGS_ERR_INVALID_ARG, "scale must be finite");
     if (W % 8 || W > 65536) return fail(FGS_ERR_UNSUPPORTED, "width must be a multiple of 8, at most 65536 (got %lld)", (long long)W);
-    if (V > 0x7FFFFFFE) return fail(FGS_ERR_UNSUPPORTED, "vocab too large (%lld)", (long long)V);
+    if (V > 1 << 28) return fail(FGS_ERR_UNSUPPORTED, "vocab too large (%lld)", (long long)V);
     if (count > 0 && (!tokens || !aligned(tokens, index_dtype == FGS_INDEX_I64 ? 8 : 4)))
         return fail(FGS_ERR_INVALID_ARG, "tokens must be an aligned device pointer");
     return FGS_OK;

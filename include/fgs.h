@@ -721,7 +721,8 @@ size_t fgs_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, i
  * out      FP32 or BF16 (out_dtype) [count x width], dense; the product is FP32,
  *          rounded once.
  * width a multiple of 8, at most 65536; strides multiples of 8 (a single row's
- * may be anything); pointers 16-byte aligned; scale finite; fewer than 2^24 tokens.
+ * may be anything); pointers 16-byte aligned; scale finite; fewer than 2^24 tokens,
+ * at most 2^28 words.
  */
 int fgs_embedding_fwd(const void *tokens, int index_dtype, int64_t count, const void *weight, int64_t ldw,
                       int weight_dtype, int64_t vocab, int64_t width, float scale, void *out, int out_dtype, void *stream);
