@@ -869,7 +869,9 @@ static int check_swiglu(int64_t rows, int64_t inter)
 {
     if (rows < 0 || inter < 0) return fail(FGS_ERR_INVALID_ARG, "rows (%lld) and inter (%lld) must be >= 0", (long long)rows, (long long)inter);
     if (inter % 8 || inter > (int64_t)1 << 30) return fail(FGS_ERR_UNSUPPORTED, "inter must be a multiple of 8, at most 2^30 (got %lld)", (long long)inter);
-    if ((rows + 15) / 16 > kMaxRowBlocks) return fail(FGS_ERR_UNSUPPORTED, "rows too large (%lld)", (long long)rows);
+    // a launch has fewer than 2^32 threads
+    if (rows > (int64_t)1 << 30 || fgs::swiglu_blocks(rows, inter) >= 1 << 24)
+        return fail(FGS_ERR_UNSUPPORTED, "rows (%lld) or inter (%lld) too large", (long long)rows, (long long)inter);
     return FGS_OK;
 }
 

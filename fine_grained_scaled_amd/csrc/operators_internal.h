@@ -96,6 +96,7 @@ struct SwigluArgs {
     int64_t ldh;
     void* dgate_up;                 // BF16 [T][2 I]
 };
+int64_t swiglu_blocks(int64_t T, int64_t I);      // workgroups of a launch
 hipError_t launch_swiglu_fwd(const SwigluArgs& a, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t stream);
 

@@ -759,7 +759,7 @@ size_t fgs_embedding_workspace_bytes(int64_t count, int64_t width);
  *          tiles first: where inter is a multiple of 128, what
  *          fgs_quantize_blockwise gives for gate_up.
  * inter and strides multiples of 8 (a single row's stride may be anything);
- * pointers 16-byte aligned; at most 1048560 rows.
+ * pointers 16-byte aligned; fewer than 2^24 blocks of 4 rows and 512 columns.
  */
 int fgs_swiglu_fwd(const void *gate_up, int64_t rows, int64_t inter, int64_t ld, void *h, uint8_t *q, float *scales,
                    void *stream);

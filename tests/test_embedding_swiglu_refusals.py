@@ -80,7 +80,8 @@ def test_swiglu_backward_invalid(how):
     assert _sbwd(**how) == _lib.FGS_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("how", [dict(I=60), dict(ld=132), dict(x=FAKE + 8), dict(q=FAKE + 8), dict(T=16 * 65535 + 1)], ids=str)
+@pytest.mark.parametrize("how", [dict(I=60), dict(ld=132), dict(x=FAKE + 8), dict(q=FAKE + 8), dict(T=1 << 26), dict(T=1 << 40),
+                                 dict(T=8192, I=1 << 23, ld=1 << 24)], ids=str)
 def test_swiglu_unsupported(how):
     assert _sfwd(**how) == _lib.FGS_ERR_UNSUPPORTED
 

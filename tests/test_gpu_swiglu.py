@@ -45,7 +45,7 @@ def _values(kept, I):
     return (codes * torch.cat([per(0), per(1)], 1)).to(F64) if T else codes.to(F64)
 
 
-SIZES = [(1, 8), (7, 2048), (16, 128), (17, 136), (33, 1000), (300, 384), (128, 5464), (5, 120)]
+SIZES = [(1, 8), (300001, 8), (3, 9000), (7, 2048), (16, 128), (17, 136), (33, 1000), (300, 384), (128, 5464), (5, 120)]
 
 
 @pytest.mark.parametrize("T, I", SIZES)
