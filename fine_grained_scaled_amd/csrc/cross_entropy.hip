@@ -37,6 +37,7 @@ namespace {
 using namespace prod;
 
 using Big = Shape<2, 4, 4, 2>;         // 256 x 256, 8 waves of 128 x 64
+using Half = Shape<2, 4, 2, 2>;        // 128 x 256: a last tile of up to 128 rows (300 tokens, 32003 x 1024: 36.4 -> 33.9 us)
 using Small = Shape<2, 4, 2, 1, 4>;    // 128 x 128, 8 waves of 64 x 32, up to 128 tokens: bound by the loads of w
 
 constexpr float LOG2E = 1.44269504088896340736f;
@@ -194,15 +195,26 @@ struct ScoreArgs {
     uint16_t* dz;                      // [rows][a piece's width] (backward)
 };
 
-template <class S>
-__device__ __forceinline__ bool score_tile(const ScoreArgs& p, f32x16 (&acc)[S::TI][S::TJ], int64_t& rows, int64_t v0,
-                                           int tiles_n, int64_t& m0, int64_t& n0, int& tn, char* smem)
+// The workgroup's tile of z: body(S{}, its place), or body(Half{}, ..) where a
+// last tile of Big has at most 128 rows.
+template <class S, class F>
+__device__ __forceinline__ void score_place(int64_t rows, int64_t v0, int tiles_n, F body)
 {
     const int tiles_m = (int)((rows + S::BM - 1) / S::BM);
-    if ((int64_t)blockIdx.x >= (int64_t)tiles_m * tiles_n) return false;
-    int tm;
+    if ((int64_t)blockIdx.x >= (int64_t)tiles_m * tiles_n) return;
+    int tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
-    m0 = (int64_t)tm * S::BM, n0 = v0 + (int64_t)tn * S::BN;
+    const int64_t m0 = (int64_t)tm * S::BM, n0 = v0 + (int64_t)tn * S::BN;
+    if constexpr (std::is_same_v<S, Big>) {
+        if (rows - m0 <= Half::BM) return body(Half{}, m0, n0, tn);
+    }
+    body(S{}, m0, n0, tn);
+}
+
+template <class S>
+__device__ __forceinline__ void score_product(const ScoreArgs& p, f32x16 (&acc)[S::TI][S::TJ], int64_t rows, int64_t m0,
+                                              int64_t n0, char* smem)
+{
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Loader<ALONG, S::BM, S::NW> la;
     Loader<ALONG, S::BN, S::NW> lb;
@@ -213,17 +225,13 @@ __device__ __forceinline__ bool score_tile(const ScoreArgs& p, f32x16 (&acc)[S::
     }, wave, lane);
     lb.rows([&](int r) { return p.w + min(n0 + r, p.V - 1) * p.ldw; }, wave, lane);
     product<S, ALONG, ALONG>(acc, la, lb, p.K, smem);
-    return true;
 }
 
 template <class S>
-__global__ __launch_bounds__(S::THREADS, 1) void ce_score_kernel(ScoreArgs p)
+__device__ __forceinline__ void score_tile(const ScoreArgs& p, int64_t rows, int64_t m0, int64_t n0, int tn, char* smem)
 {
-    extern __shared__ __align__(256) char smem[];
     f32x16 acc[S::TI][S::TJ];
-    int64_t rows = p.r.count ? *p.r.count : p.T, m0, n0;
-    int tn;
-    if (!score_tile<S>(p, acc, rows, 0, p.tiles_n, m0, n0, tn, smem)) return;
+    score_product<S>(p, acc, rows, m0, n0, smem);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int wm = wave / S::NWN, wn = wave % S::NWN;
     const int64_t nw = n0 + wn * S::WN;
@@ -282,6 +290,16 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_score_kernel(ScoreArgs p)
         }
         if (m0 + row < rows) p.part[(int64_t)tn * p.Tp + m0 + row] = make_float2(top, sum);
     }
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS, 1) void ce_score_kernel(ScoreArgs p)
+{
+    extern __shared__ __align__(256) char smem[];
+    const int64_t rows = p.r.count ? *p.r.count : p.T;
+    score_place<S>(rows, 0, p.tiles_n, [&](auto shape, int64_t m0, int64_t n0, int tn) {
+        score_tile<decltype(shape)>(p, rows, m0, n0, tn, smem);
+    });
 }
 
 // Every token's loss and lse from its row's parts: 16 rows a workgroup, 64
@@ -373,14 +391,11 @@ __device__ __forceinline__ void store_tile(char* smem, F f, W write)
 
 // A tile of dz: z again, then the softmax from the row's lse.
 template <class S>
-__global__ __launch_bounds__(S::THREADS, 1) void ce_gradient_kernel(ScoreArgs p)
+__device__ __forceinline__ void gradient_tile(const ScoreArgs& p, int64_t rows, int64_t v0, int64_t m0, int64_t n0, char* smem)
 {
-    extern __shared__ __align__(256) char smem[];
     f32x16 acc[S::TI][S::TJ];
-    const Piece at = piece_of(p.r, p.piece, p.V);
-    int64_t rows = p.r.count[0], m0, n0;
-    int tn;
-    if (!score_tile<S>(p, acc, rows, at.v0, (int)(at.padded / S::BN), m0, n0, tn, smem)) return;
+    score_product<S>(p, acc, rows, m0, n0, smem);
+    const int64_t ld = p.r.count[1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int wm = wave / S::NWN, wn = wave % S::NWN;
     const int64_t nw = n0 + wn * S::WN;
@@ -411,7 +426,18 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_gradient_kernel(ScoreArgs p)
         }
     }
     store_tile<S>(smem, [&](int i, int j, int k) { return acc[i][j][k]; },
-                  [&](int row, int c) { return p.dz + (m0 + row) * at.ld + (n0 - at.v0) + 8 * c; });
+                  [&](int row, int c) { return p.dz + (m0 + row) * ld + (n0 - v0) + 8 * c; });
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS, 1) void ce_gradient_kernel(ScoreArgs p)
+{
+    extern __shared__ __align__(256) char smem[];
+    const Piece at = piece_of(p.r, p.piece, p.V);
+    const int64_t rows = p.r.count[0];
+    score_place<S>(rows, at.v0, (int)(at.padded / S::BN), [&](auto shape, int64_t m0, int64_t n0, int) {
+        gradient_tile<decltype(shape)>(p, rows, at.v0, m0, n0, smem);
+    });
 }
 
 struct GradArgs {
