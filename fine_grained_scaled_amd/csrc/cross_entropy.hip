@@ -36,9 +36,17 @@ namespace {
 
 using namespace prod;
 
-using Big = Shape<2, 4, 4, 2>;         // 256 x 256, 8 waves of 128 x 64
-using Half = Shape<2, 4, 2, 2>;        // 128 x 256: a last tile of up to 128 rows (300 tokens, 32003 x 1024: 36.4 -> 33.9 us)
-using Small = Shape<2, 4, 2, 1, 4>;    // 128 x 128, 8 waves of 64 x 32, up to 128 tokens: bound by the loads of w
+// 256 x 256, 8 waves of 128 x 64 (4 waves of 128 x 128, 8192 tokens: 29.4 ms for
+// 28.4).  An operand that is read along its rows comes in whole lines of 128
+// bytes with stages of 64 values, two of them; with four of 32 the copies start
+// a stage earlier, which pays where no operand is (dw: 841 us a piece for 869,
+// the scores 7180 for 6910).
+using Big = Shape<2, 4, 4, 2, 64, 2>;
+using Deep = Shape<2, 4, 4, 2, 32, 4>;
+// 128 x 256: a last tile of up to 128 rows (300 tokens, 32003 x 1024: 33.9 us for 36.4)
+using Half = Shape<2, 4, 2, 2, 64, 2>;
+// 128 x 128, up to 128 tokens: bound by the loads of w
+using Small = Shape<2, 4, 2, 1, 64, 4>;
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
@@ -216,8 +224,8 @@ __device__ __forceinline__ void score_product(const ScoreArgs& p, f32x16 (&acc)[
                                               int64_t n0, char* smem)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    Loader<ALONG, S::BM, S::NW> la;
-    Loader<ALONG, S::BN, S::NW> lb;
+    Loader<ALONG, S::BM, S::NW, S::BK> la;
+    Loader<ALONG, S::BN, S::NW, S::BK> lb;
     la.rows([&](int r) {
         int64_t row = min(m0 + r, rows - 1);
         if (p.r.token) row = p.r.token[row];
@@ -463,12 +471,12 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_dx_kernel(GradArgs p)
     const int split = (int)(blockIdx.x / each);
     int tm, tn;
     tile_of(blockIdx.x - split * each, tiles_m, p.tiles_n, tm, tn);
-    const int64_t per = up((at.padded + splits - 1) / splits, BK);
+    const int64_t per = up((at.padded + splits - 1) / splits, S::BK);
     const int64_t m0 = (int64_t)tm * S::BM, n0 = (int64_t)tn * S::BN, k0 = split * per;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t values = max((int64_t)0, min(per, at.width - k0));
-    Loader<ALONG, S::BM, S::NW> la;
-    Loader<ACROSS, S::BN, S::NW> lb;
+    Loader<ALONG, S::BM, S::NW, S::BK> la;
+    Loader<ACROSS, S::BN, S::NW, S::BK> lb;
     la.rows([&](int r) { return p.dz + (m0 + r) * at.ld + k0; }, wave, lane);
     lb.columns(p.w + min(at.v0 + k0, p.V - 1) * p.ldw, p.ldw, n0, p.K, wave, lane);
     f32x16 acc[S::TI][S::TJ];
@@ -535,12 +543,12 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_dw_kernel(GradArgs p)
     tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = (int64_t)tm * S::BM, n0 = (int64_t)tn * S::BN;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    Loader<ACROSS, S::BM, S::NW> la;
-    Loader<ACROSS, S::BN, S::NW> lb;
+    Loader<ACROSS, S::BM, S::NW, S::BK> la;
+    Loader<ACROSS, S::BN, S::NW, S::BK> lb;
     la.columns(p.dz, at.ld, m0, at.ld, wave, lane);
     lb.columns(p.xc, p.K, n0, p.K, wave, lane);
     f32x16 acc[S::TI][S::TJ];
-    product<S, ACROSS, ACROSS>(acc, la, lb, up(rows, BK), smem);
+    product<S, ACROSS, ACROSS>(acc, la, lb, up(rows, 64), smem);
     const float scale = *p.r.most;
     store_tile<S>(smem, [&](int i, int j, int k) { return acc[i][j][k] * scale; },
                   [&](int row, int c) -> uint16_t* {
@@ -691,7 +699,7 @@ static hipError_t backward(const CrossEntropyArgs& c, Plan& p, hipStream_t strea
         if (hipError_t e = go<S>(ce_dx_kernel<S>, p.cut.slots, g, stream); e != hipSuccess) return e;
         // (the first piece may be all of the vocabulary, a later one is no wider than the rest)
         const int64_t rest = up(c.V - i * piece_width(p.cut, p.Tp), 256);
-        if (hipError_t e = go<Big>(ce_dw_kernel<Big>, rest / Big::BM * (up(c.K, Big::BN) / Big::BN), g, stream); e != hipSuccess) return e;
+        if (hipError_t e = go<Deep>(ce_dw_kernel<Deep>, rest / Deep::BM * (up(c.K, Deep::BN) / Deep::BN), g, stream); e != hipSuccess) return e;
     }
     if (c.T == 0) return hipSuccess;
     ce_dx_store_kernel<S><<<(uint32_t)(tiles_m * g.tiles_n * (S::BM * S::BN / 8 / 256)), 256, 0, stream>>>(g);

@@ -27,13 +27,12 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef __attribute__((address_space(3))) s16x4* lds_v4;
 typedef const __attribute__((address_space(3))) bf16x8* lds_v8;
 
-constexpr int BK = 64;                       // contraction values a stage
-
 enum Side { ALONG, ACROSS };                 // the contraction runs along an operand's rows, or across them
 
-template <int NWM_, int NWN_, int TI_, int TJ_, int STAGES_ = 2>
+// (BK: contraction values a stage)
+template <int NWM_, int NWN_, int TI_, int TJ_, int BK_, int STAGES_>
 struct Shape {
-    static constexpr int NWM = NWM_, NWN = NWN_, TI = TI_, TJ = TJ_, STAGES = STAGES_;
+    static constexpr int NWM = NWM_, NWN = NWN_, TI = TI_, TJ = TJ_, BK = BK_, STAGES = STAGES_;
     static_assert((STAGES & (STAGES - 1)) == 0, "a stage's place is its number's low bits");
     static constexpr int NW = NWM * NWN, THREADS = 64 * NW;
     static constexpr int WM = 32 * TI, WN = 32 * TJ;                 // a wave's part of the tile
@@ -81,26 +80,27 @@ __device__ __forceinline__ void publish()
 
 // 16-byte chunk c of staged row r sits in slot c ^ f(r): 16 rows of one chunk
 // (ALONG), or 4 rows of 4 neighbouring chunks (ACROSS), touch every bank once.
-template <Side SIDE, int EXT>
+template <Side SIDE, int EXT, int BK>
 __device__ __forceinline__ constexpr uint32_t swizzle(uint32_t r)
 {
-    return SIDE == ALONG ? (r >> 1) & 7 : EXT >= 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+    static_assert(BK == 32 || BK == 64, "rows of 64 or 128 bytes");
+    return SIDE == ALONG ? (BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3) : EXT >= 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
 }
 
 // One operand's copies: EXT rows (ALONG) or columns (ACROSS) of the tile.
-template <Side SIDE, int EXT, int NW>
+template <Side SIDE, int EXT, int NW, int BK>
 struct Loader {
-    static constexpr int SLOTS = SIDE == ALONG ? 8 : EXT / 8;        // chunks a staged row
+    static constexpr int SLOTS = SIDE == ALONG ? BK / 8 : EXT / 8;   // chunks a staged row
     static constexpr int PER = 64 / SLOTS;                           // staged rows a copy
-    static constexpr int N = EXT / 8 / NW;                           // copies a wave and stage
-    static_assert(N * NW * 8 == EXT && PER * SLOTS == 64, "whole copies");
+    static constexpr int N = EXT * BK / 512 / NW;                    // copies a wave and stage
+    static_assert(N * NW * 512 == EXT * BK && PER * SLOTS == 64, "whole copies");
     const char* at[N];
     int64_t ld;                                                      // bytes (ACROSS)
 
     __device__ __forceinline__ static int row(int wave, int lane, int j) { return (wave * N + j) * PER + lane / SLOTS; }
     __device__ __forceinline__ static int chunk(int wave, int lane, int j)
     {
-        return (lane % SLOTS) ^ swizzle<SIDE, EXT>(row(wave, lane, j));
+        return (lane % SLOTS) ^ swizzle<SIDE, EXT, BK>(row(wave, lane, j));
     }
     // ALONG: where(r) is row r's first contraction value
     template <class F>
@@ -137,18 +137,18 @@ struct Loader {
 };
 
 // The operand fragment of values 16 ks .. 16 ks + 15 of the stage and rows
-// (columns) first + l % 32 of the tile; address: fragment<>() of the lane.
-template <Side SIDE, int EXT>
+// (columns) first + l % 32 of the tile; address: fragment_address() of the lane.
+template <Side SIDE, int EXT, int BK>
 __device__ __forceinline__ uint32_t fragment_address(int first, int lane)
 {
     if constexpr (SIDE == ALONG) {
         const uint32_t r = first + (lane & 31);
-        return r * (2 * BK) + (((uint32_t)(lane >> 5) ^ swizzle<ALONG, EXT>(lane & 31)) << 4);
+        return r * (2 * BK) + (((uint32_t)(lane >> 5) ^ swizzle<ALONG, EXT, BK>(lane & 31)) << 4);
     } else {
         const int i = lane & 15;
         const uint32_t r = 8 * (lane >> 5) + (i >> 2);
         const uint32_t c = first / 8 + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-        return r * (2 * EXT) + ((c ^ swizzle<ACROSS, EXT>(r)) << 4) + 8 * (i & 1);
+        return r * (2 * EXT) + ((c ^ swizzle<ACROSS, EXT, BK>(r)) << 4) + 8 * (i & 1);
     }
 }
 template <Side SIDE, int EXT>
@@ -169,9 +169,10 @@ __device__ __forceinline__ bf16x8 fragment(uint32_t address, uint32_t tile, int 
 // meets with zeros).  smem: S::LDS bytes, free again for every wave after the
 // call.
 template <class S, Side SA, Side SB>
-__device__ __forceinline__ void product(f32x16 (&acc)[S::TI][S::TJ], Loader<SA, S::BM, S::NW>& la,
-                                        Loader<SB, S::BN, S::NW>& lb, int64_t values, char* smem)
+__device__ __forceinline__ void product(f32x16 (&acc)[S::TI][S::TJ], Loader<SA, S::BM, S::NW, S::BK>& la,
+                                        Loader<SB, S::BN, S::NW, S::BK>& lb, int64_t values, char* smem)
 {
+    constexpr int BK = S::BK, KS = BK / 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::NWN, wn = wave % S::NWN;
     const uint32_t lds = lds_offset(smem);
@@ -183,13 +184,14 @@ __device__ __forceinline__ void product(f32x16 (&acc)[S::TI][S::TJ], Loader<SA, 
     if (steps == 0) return;
     uint32_t aa[S::TI], ab[S::TJ];
 #pragma unroll
-    for (int i = 0; i < S::TI; ++i) aa[i] = fragment_address<SA, S::BM>(wm * S::WM + 32 * i, lane);
+    for (int i = 0; i < S::TI; ++i) aa[i] = fragment_address<SA, S::BM, BK>(wm * S::WM + 32 * i, lane);
 #pragma unroll
-    for (int j = 0; j < S::TJ; ++j) ab[j] = fragment_address<SB, S::BN>(wn * S::WN + 32 * j, lane);
+    for (int j = 0; j < S::TJ; ++j) ab[j] = fragment_address<SB, S::BN, BK>(wn * S::WN + 32 * j, lane);
 
     bf16x8 fa[2][S::TI], fb[2][S::TJ];
     constexpr int READS = S::TI + S::TJ, MMAS = S::TI * S::TJ;
-    constexpr int AHEAD = S::STAGES - 1, A_COPIES = Loader<SA, S::BM, S::NW>::N, COPIES = A_COPIES + Loader<SB, S::BN, S::NW>::N;
+    constexpr int A_COPIES = Loader<SA, S::BM, S::NW, BK>::N,
+                  COPIES = A_COPIES + Loader<SB, S::BN, S::NW, BK>::N;
     auto place = [&](int step) { return lds + (step & (S::STAGES - 1)) * S::STAGE; };
     auto read = [&](int f, int set, uint32_t stage, int ks) {
         if (f < S::TI) fa[set][f] = fragment<SA, S::BM>(aa[f], stage, ks);
@@ -209,37 +211,32 @@ __device__ __forceinline__ void product(f32x16 (&acc)[S::TI][S::TJ], Loader<SA, 
         else lb.issue(c - A_COPIES, place(step) + S::A_BYTES, wave);
     };
 #pragma unroll
-    for (int step = 0; step < AHEAD; ++step)
+    for (int step = 0; step < S::STAGES; ++step)
         if (step < steps)
 #pragma unroll
             for (int c = 0; c < COPIES; ++c) copy(c, step);
-    if (AHEAD > 1 && steps >= AHEAD) publish<(AHEAD - 1) * COPIES>();
+    if (steps >= S::STAGES) publish<(S::STAGES - 1) * COPIES>();
     else publish<0>();
 #pragma unroll
     for (int f = 0; f < READS; ++f) read(f, 0, lds, 0);
     // The order below is kept as it is written: a fragment is read a whole
     // k-step before its products, and a copy starts beside a product, so that
     // neither is waited for (left to the compiler, reads stand right before
-    // their products).
-    // fill: the stage AHEAD of this one is copied, every wave being past its
-    // reads of the place; more: there is a next stage
+    // their products).  The stage's last products run after the barrier that
+    // publishes the next stage, beside that stage's first reads and, every wave
+    // being past its reads of this one, the copies that take its place.
+    // fill: there are such copies; more: there is a next stage.
     auto advance = [&](int step, auto fill, auto more) {
 #pragma unroll
-        for (int ks = 0; ks < 3; ++ks)
+        for (int ks = 0; ks < KS - 1; ++ks)
 #pragma unroll
             for (int t = 0; t < MMAS; ++t) {
                 multiply(t, ks & 1);
 #pragma unroll
                 for (int f = t * READS / MMAS; f < (t + 1) * READS / MMAS; ++f) read(f, (ks + 1) & 1, place(step), ks + 1);
-                if constexpr (fill) {
-                    if (ks == 0)
-#pragma unroll
-                        for (int c = t * COPIES / MMAS; c < (t + 1) * COPIES / MMAS; ++c) copy(c, step + AHEAD);
-                }
                 __builtin_amdgcn_sched_barrier(0);
             }
-        // the stage's last products run after the barrier, beside the next stage's first reads
-        publish<fill ? (AHEAD - 1) * COPIES : 0>();
+        publish<fill ? (S::STAGES - 2) * COPIES : 0>();
 #pragma unroll
         for (int t = 0; t < MMAS; ++t) {
             multiply(t, 1);
@@ -247,11 +244,15 @@ __device__ __forceinline__ void product(f32x16 (&acc)[S::TI][S::TJ], Loader<SA, 
 #pragma unroll
                 for (int f = t * READS / MMAS; f < (t + 1) * READS / MMAS; ++f) read(f, 0, place(step + 1), 0);
             }
+            if constexpr (fill) {
+#pragma unroll
+                for (int c = t * COPIES / MMAS; c < (t + 1) * COPIES / MMAS; ++c) copy(c, step + S::STAGES);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     int step = 0;
-    for (; step < steps - AHEAD; ++step) advance(step, std::true_type{}, std::true_type{});
+    for (; step < steps - S::STAGES; ++step) advance(step, std::true_type{}, std::true_type{});
     for (; step < steps - 1; ++step) advance(step, std::false_type{}, std::true_type{});
     advance(step, std::false_type{}, std::false_type{});
 }
