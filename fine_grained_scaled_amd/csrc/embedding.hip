@@ -21,6 +21,11 @@
 // of one that spans pieces go to the workspace, and a last kernel adds them in
 // a fixed order.  The rows that no token is get their zeros from workgroups of
 // their own in the launch that sums, so each row of dw is written once.
+//
+// Measured: 16381 rows of 7168 FP32 values 160 us (5.9 TB/s); gradient of 8192
+// tokens, 128000 x 4096 FP32, 423 us, 395 of them the launch that sums and clears
+// (5.3 TB/s written), the sort 12; 61440 tokens, 70% of them the same, 32003 x 1024
+// BF16 from FP32, 109 us: the sums 60, the sort 26, the long sum's parts 14.
 #include <algorithm>
 #include <climits>
 

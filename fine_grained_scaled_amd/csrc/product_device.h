@@ -9,6 +9,10 @@
 // of 128 bytes and read 16 bytes a lane; one whose contraction runs across its
 // rows as 64 rows of BM (or BN) values, read by the transposing loads, so no
 // operand has to be transposed in memory first.
+//
+// Bound by the matrix units: 8192 x 128000 over 4096 values 6.37 ms (1.35
+// PFLOP/s, 73% busy, on a card where the library's product of 8192^3 reaches
+// 1.40), both operands read along their rows; 6.31 ms with both across them.
 #pragma once
 
 #include <type_traits>

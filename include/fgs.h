@@ -663,6 +663,12 @@ int fgs_clip_grad_norm(const fgs_grad *grads, int32_t count, float max_norm, flo
                        void *workspace, size_t workspace_bytes, void *stream);
 size_t fgs_clip_workspace_bytes(int32_t count);
 
+/*
+ * The two ends of a model and its MLP's activation: the output head with
+ * softmax cross entropy, token embedding, and SwiGLU with its input kept in 8
+ * bits for the backward pass.
+ */
+
 /* Token ids and targets. */
 enum { FGS_INDEX_I32 = 0, FGS_INDEX_I64 = 1 };
 
