@@ -266,16 +266,15 @@ __device__ __forceinline__ void score_tile(const ScoreArgs& p, int64_t rows, int
 #pragma unroll
             for (int k = 0; k < 16; ++k) top = fmaxf(top, acc[i][j][k]);
         top = fmaxf(top, swap_half(top));
-        // 2^(z log2 e - base), one multiply-add an exponent; what base's rounding
-        // takes from top log2 e comes back as a factor of the sum
-        const float base = (top == -INFINITY ? 0.0f : top) * LOG2E;
+        // the distance first, then log2 e: z log2 e by itself is off by up to 2^-24 of its size, from 2^31 on more than
+        // an exponent holds (one multiply-add a score instead: 4099 tokens, 50021 x 2048 760 us for 764)
+        const float base = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < S::TJ; ++j)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], LOG2E, -base));
+            for (int k = 0; k < 16; ++k) sum += __builtin_amdgcn_exp2f((acc[i][j][k] - base) * LOG2E);
         sum += swap_half(sum);
-        if (top != -INFINITY) sum *= __builtin_amdgcn_exp2f(__builtin_fmaf(-top, LOG2E, base));
         if (half == 0) red[wn * S::BM + row] = make_float2(top, sum);
         // the target's value, from the lane that holds it
         int target = -1;
@@ -415,12 +414,12 @@ __device__ __forceinline__ void gradient_tile(const ScoreArgs& p, int64_t rows, 
 #pragma unroll
     for (int i = 0; i < S::TI; ++i) {
         const int64_t row = m0 + wm * S::WM + 32 * i + (lane & 31);      // within the padded rows
-        const float lse = p.r.lse[row] * LOG2E, b = p.r.dloss[row] / most, a = b + p.r.dlse[row] / most;
+        const float lse = p.r.lse[row], b = p.r.dloss[row] / most, a = b + p.r.dlse[row] / most;
         const int64_t in = p.r.target[row] - nw;
 #pragma unroll
         for (int j = 0; j < S::TJ; ++j)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) acc[i][j][k] = a * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], LOG2E, -lse));
+            for (int k = 0; k < 16; ++k) acc[i][j][k] = a * __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * LOG2E);
         if (__any(in >= 0 && in < S::WN)) {
 #pragma unroll
             for (int j = 0; j < S::TJ; ++j)

@@ -687,7 +687,8 @@ enum { FGS_INDEX_I32 = 0, FGS_INDEX_I64 = 1 };
  * targets  DEVICE int32 or int64 (index_dtype FGS_INDEX_*) [tokens].
  * loss, lse  FP32 [tokens].
  * Products are exact and summed in FP32, as are exponents.  A row whose
- * logits hold NaN or +Inf has loss and lse NaN.
+ * logits hold NaN or +Inf has loss and lse NaN; any finite logits have finite
+ * ones where the values are.
  * workspace  DEVICE scratch, 16-byte aligned, of at least
  *   fgs_linear_cross_entropy_workspace_bytes(tokens, vocab, width, 0) bytes.
  */
@@ -705,7 +706,9 @@ int fgs_linear_cross_entropy_fwd(const void *x, int64_t ldx, const void *w, int6
  * dw       BF16 [vocab x width], dense.
  * The logits are formed again, a piece of the vocabulary at a time.  dz is
  * rounded to BF16 for the two products, after division by the largest |dloss|
- * or |dlse| of the tokens with a target; sums are FP32, in a fixed order.
+ * or |dlse| of the tokens with a target; sums are FP32, in a fixed order.  lse
+ * is what FP32 holds of it: exp(z - lse) is off by up to 2^-24 |lse| of itself
+ * where several words share the probability.
  * workspace  DEVICE scratch, 16-byte aligned, of at least
  *   fgs_linear_cross_entropy_workspace_bytes(tokens, vocab, width, 1) bytes.
  */
