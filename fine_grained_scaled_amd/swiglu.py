@@ -16,11 +16,20 @@ def _halves(cols: int) -> int:
     return cols // 2
 
 
+class _Halves(Quantized):
+    """Codes of [g | u] whose halves end inside a tile: the scales belong to
+    the halves' tiles and not to those of whole rows, which a GEMM reads."""
+
+    def rowwise(self):
+        raise ValueError("SwiGLU's codes are a GEMM operand only where its halves are whole tiles of 128 columns")
+
+
 def swiglu_fwd(gate_up: torch.Tensor, checkpoint: bool = True):
     """h = g sigmoid(g) u of gate_up = [g | u], bfloat16 [T x 2I] (I a
     multiple of 8): returns (h [T x I], kept), kept being gate_up's 1x128
-    E4M3 quantization, half by half, for swiglu_bwd (half of gate_up's bytes),
-    or None without checkpoint."""
+    E4M3 quantization, half by half, for swiglu_bwd (half of gate_up's bytes;
+    an operand of a GEMM too where I is a multiple of 128), or None without
+    checkpoint."""
     T, cols, ld = _bf16_matrix(gate_up)
     inter = _halves(cols)
     h = gate_up.new_empty(T, inter)
@@ -31,7 +40,9 @@ def swiglu_fwd(gate_up: torch.Tensor, checkpoint: bool = True):
     _lib.check(_lib.load().fgs_swiglu_fwd(
         gate_up.data_ptr(), T, inter, ld, h.data_ptr(), q.data_ptr() if checkpoint else 0,
         scales.data_ptr() if checkpoint else 0, _stream_of(gate_up)))
-    return h, Quantized(q, scales, None, None, _lib.SCALE_TILE_1x128) if checkpoint else None
+    if not checkpoint:
+        return h, None
+    return h, (_Halves if inter % 128 else Quantized)(q, scales, None, None, _lib.SCALE_TILE_1x128)
 
 
 def swiglu_bwd(dh: torch.Tensor, kept: Union[Quantized, torch.Tensor]) -> torch.Tensor:
