@@ -92,7 +92,8 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, targets):
         ctx.w_dtype, ctx.x_dtype = w.dtype, x.dtype
-        x, w = _readable(x.to(torch.bfloat16), x.shape[1]), _readable(w.to(torch.bfloat16), w.shape[1])
+        x, w = _readable(x.to(torch.bfloat16), x.shape[-1]), _readable(w.to(torch.bfloat16), w.shape[-1])
+        targets = targets.contiguous()
         loss, lse = linear_cross_entropy_fwd(x, w, targets)
         ctx.save_for_backward(x, w, targets, lse)
         return loss, lse
@@ -108,7 +109,8 @@ class _LinearCrossEntropy(torch.autograd.Function):
 def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, return_lse: bool = False):
     """linear_cross_entropy_fwd's loss for each token, float32 [T], with
     autograd: gradients for x and w.  w is BF16 or an FP32 master weight (its
-    BF16 cast is multiplied, its gradient comes in its own type).  return_lse:
-    (loss, lse), both with gradients, for a penalty on lse."""
+    BF16 cast is multiplied, its gradient comes in its own type).  Layouts that
+    the kernels do not read are copied.  return_lse: (loss, lse), both with
+    gradients, for a penalty on lse."""
     loss, lse = _LinearCrossEntropy.apply(x, w, targets)
     return (loss, lse) if return_lse else loss

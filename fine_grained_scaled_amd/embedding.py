@@ -30,7 +30,7 @@ def embedding_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0
                   out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """scale * weight[tokens], [*tokens.shape x width] in out_dtype (float32
     or bfloat16; the weight's type unless given), zeros for tokens outside
-    [0, vocab).  tokens: int32 or int64 of any shape; weight [vocab x width]
+    [0, vocab).  tokens: int32 or int64 of any shape, contiguous; weight [vocab x width]
     float32 or bfloat16, width a multiple of 8."""
     index = _tokens(tokens)
     kind = _type(weight.dtype, "weight")
@@ -88,6 +88,7 @@ def embedding_bwd(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, scale: f
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale, out_dtype):
+        tokens, weight = tokens.contiguous(), _readable(weight, weight.shape[-1])
         ctx.save_for_backward(tokens)
         ctx.vocab, ctx.scale, ctx.dtype = weight.shape[0], scale, weight.dtype
         return embedding_fwd(tokens, weight, scale, out_dtype)
@@ -103,5 +104,6 @@ class _Embedding(torch.autograd.Function):
 
 def embedding(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-    """embedding_fwd with autograd: a gradient for the weight, in its type."""
+    """embedding_fwd with autograd: a gradient for the weight, in its type.
+    Layouts that the kernels do not read are copied."""
     return _Embedding.apply(tokens, weight, scale, out_dtype)

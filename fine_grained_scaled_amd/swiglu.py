@@ -73,6 +73,7 @@ def swiglu_bwd(dh: torch.Tensor, kept: Union[Quantized, torch.Tensor]) -> torch.
 class _Swiglu(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate_up, checkpoint):
+        gate_up = _readable(gate_up, gate_up.shape[-1])
         h, kept = swiglu_fwd(gate_up, checkpoint)
         ctx.checkpoint = checkpoint
         ctx.save_for_backward(*((kept.q, kept.scales) if checkpoint else (gate_up,)))
@@ -89,5 +90,6 @@ class _Swiglu(torch.autograd.Function):
 def swiglu(gate_up: torch.Tensor, checkpoint: bool = True) -> torch.Tensor:
     """swiglu_fwd's h with autograd.  checkpoint: what the backward pass
     needs of gate_up is kept in 8 bits, so gate_up itself need not be
-    (False: it is kept as it is)."""
+    (False: it is kept as it is).  Layouts that the kernels do not read are
+    copied."""
     return _Swiglu.apply(gate_up, checkpoint)
