@@ -135,7 +135,7 @@ struct SortArgs {
 
 __global__ __launch_bounds__(1024) void embedding_sort_kernel(SortArgs p)
 {
-    __shared__ int s_key[CHUNK];
+    __shared__ __align__(16) int s_key[CHUNK];       // read four at a time
     __shared__ int s_rank[TABLE];
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
