@@ -39,9 +39,10 @@ __device__ __forceinline__ uint32_t bf16x2_rne(float a, float b)
 }
 
 // sigmoid(g) = root^2 one and 1 - sigmoid(g) = rest, within a few FP32 steps.
-// The factors are products of two with the root on each side, so that nothing
-// underflows before the product does: exp(-|g|) alone leaves FP32's normal
-// numbers at 87.
+// The factors are products of two with the root on each side, so that neither
+// underflows before the product does where they are alike: exp(-|g|) alone leaves
+// FP32's normal numbers at 87.  one (and the slope) go to the first of the two,
+// so that nothing overflows before the product does.
 __device__ __forceinline__ void sigmoid(float g, float& root, float& one, float& rest)
 {
     const float t = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * (0.5f * LOG2E)), e = t * t;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(SwigluArgs p)
         for (int k = 0; k < 8; ++k) {
             float root, one, rest;
             sigmoid(a[k], root, one, rest);
-            a[k] = (a[k] * root) * (b[k] * root) * one;
+            a[k] = (a[k] * root * one) * (b[k] * root);
         }
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h) + row * p.I + col) = pack(a);
     }
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluArgs p)
         float root, one, rest;
         sigmoid(g[k], root, one, rest);
         const float ds = d[k] * root * one;
-        const float dg = ds * (u[k] * root) * __builtin_fmaf(g[k], rest, 1.0f);
+        const float dg = (ds * __builtin_fmaf(g[k], rest, 1.0f)) * (u[k] * root);
         u[k] = ds * (g[k] * root);
         g[k] = dg;
     }

@@ -760,7 +760,7 @@ size_t fgs_embedding_workspace_bytes(int64_t count, int64_t width);
  *   backward pass: h = g sigmoid(g) u of gate_up = [g | u].
  * gate_up  BF16 [rows x 2*inter], row stride ld: g = columns 0..inter-1, u the
  *          others.  h: BF16 [rows x inter], dense, within one BF16 ulp of the exact
- *          value (results below 2^-120 may be 0).
+ *          value (results below 2^-116 may be 0).
  * q, scales  NULL, or the kept input: the 1x128 quantization of each half ([DSV3]
  *          "Fine-grained quantization", "Online quantization"; inter need not be a
  *          multiple of 128: a half's last tile is shorter then).  q E4M3
@@ -778,8 +778,10 @@ int fgs_swiglu_fwd(const void *gate_up, int64_t rows, int64_t inter, int64_t ld,
  *   stride lddh) and the kept input:
  *     dg = dh u sigmoid(g) (1 + g (1 - sigmoid(g))),  du = dh g sigmoid(g)
  *   at the values that q and scales stand for (gate_up NULL), or at gate_up
- *   itself (q NULL).  dgate_up: BF16 [rows x 2*inter], dense.  A tile that held
- *   NaN or Inf was kept as NaN: all of its gradients are NaN.
+ *   itself (q NULL).  dgate_up: BF16 [rows x 2*inter], dense, FP32 products rounded
+ *   once; for g < 0 so where |g| is below 174 and dh exp(g / 2)
+ *   and u exp(g / 2) are normal FP32 numbers, and smaller or 0 elsewhere.  A tile
+ *   that held NaN or Inf was kept as NaN: all of its gradients are NaN.
  */
 int fgs_swiglu_bwd(const void *dh, int64_t lddh, const void *gate_up, int64_t ld, const uint8_t *q, const float *scales,
                    int64_t rows, int64_t inter, void *dgate_up, void *stream);
