@@ -109,7 +109,8 @@ class _LinearCrossEntropy(torch.autograd.Function):
 def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, return_lse: bool = False):
     """linear_cross_entropy_fwd's loss for each token, float32 [T], with
     autograd: gradients for x and w.  w is BF16 or an FP32 master weight (its
-    BF16 cast is multiplied, its gradient comes in its own type).  Layouts that
+    BF16 cast is multiplied; its gradient is rounded to BF16 as a BF16 weight's
+    is, and cast to its type).  Both gradients are formed.  Layouts that
     the kernels do not read are copied.  return_lse: (loss, lse), both with
     gradients, for a penalty on lse."""
     loss, lse = _LinearCrossEntropy.apply(x, w, targets)

@@ -26,9 +26,10 @@
 // mean over the tokens the values are then softmax - onehot itself, whose
 // largest, those of the targets, round best (-1 exactly).
 //
-// Measured: 8192 tokens, 128000 x 4096, forward and backward 26.2 ms, 8 T V K
-// operations at 1.31 PFLOP/s; 4099 tokens, 50021 x 2048 forward 728 us; 5 tokens,
-// 32003 x 512 forward 12.6 us, of which reading w takes 8.6.
+// Measured, the fastest card to the slowest: 8192 tokens, 128000 x 4096, forward
+// and backward 26.2 to 27.6 ms, 8 T V K operations at 1.31 to 1.25 PFLOP/s; 4099
+// tokens, 50021 x 2048 forward 728 to 799 us; 5 tokens, 32003 x 512 forward 12.7 us,
+// of which the kernel that reads w takes 9.0.
 #include <algorithm>
 #include <cmath>
 
@@ -88,9 +89,12 @@ __host__ __device__ inline int64_t piece_width(const Cut& c, int64_t rows)
 }
 
 // Workgroups that share a tile of dx, each a part of the piece: the fewest
-// microseconds.  A step of 64 values takes a compute unit 1.9 us per 256 x 256
-// (measured: 1.15 PFLOP/s); a part's sums are read and written again, 0.117 us
-// of the chip's time (512 KiB at 4.5 TB/s).
+// microseconds.  A step of 64 values is taken to cost a compute unit 1.9 us per
+// 256 x 256 and a part's first loads 3 us; its sums are read and written again,
+// 0.117 us of the chip's time (512 KiB at 4.5 TB/s).  The present main loop takes
+// 1.53 us a step and 1.5 us besides its sums (4096 tokens, 2048 to 16384 words x
+// 4096: 65 to 409 us): with these the choice differs at 100 of 2808 sizes from 1
+// to 32768 tokens, by at most 2% of the time.  A 128 x 128 tile counts as a quarter.
 // (By the 64 lanes of a wave.)
 __device__ inline int dx_splits(const Cut& c, int64_t rows, int64_t width)
 {
@@ -564,12 +568,18 @@ __global__ __launch_bounds__(S::THREADS, 1) void ce_dw_kernel(GradArgs p)
 // would be padding for the most part: 128 x 128 with three stages on their way
 // takes 64 us for 100 tokens, 32000 x 4096 forward (107 with 256 x 256), 207 for
 // 128 tokens, 128000 x 4096 (252).  (64 x 128 in 4 waves: 2% less at 5 tokens,
-// 14 to 30% more from 65 on.)
+// 14 to 30% more from 65 on.)  Above, 256 x 256 pays from 257 tokens on and not
+// yet at 129 to 256, where two rows of 128 x 128 tiles would take less: 32000 x
+// 4096 forward 101 us for 84 at 129 tokens and 108 for 91 at 256, then 105 for 120
+// at 257 and 179 for 200 at 600; forward and backward 406 for 349, 428 for 388,
+// and 479 for 499 at 300; 32003 x 1024 forward 28 for 25 at 129, 34 for 38 at 257.
 constexpr int64_t SMALL = Small::BM;
 // dz of one piece of the vocabulary: 256 MiB, or 8192 words where that is more.
 constexpr int64_t PIECE_VALUES = (int64_t)1 << 27, PIECE_LEAST = 8192;
 // Parts of dx: sums of 1280 tiles at most, where their number is not more
-// already, and 1024 values of the contraction each at least.
+// already, and one for each 1024 words of the vocabulary at most (of one piece that
+// is 1024 values of the contraction each at least; where there are several, the
+// times above choose no shorter ones at any of those 2808 sizes).
 constexpr int64_t SLOTS = 1280, PART_LEAST = 1024;
 
 // The workspace's parts, each at a multiple of 256 bytes.

@@ -19,7 +19,7 @@
 // that one token in most positions (padding) is summed by as many workgroups as
 // any other input.  A sum that lies in one piece is written at once; the parts
 // of one that spans pieces go to the workspace, and a last kernel adds them in
-// a fixed order.  The rows that no token is get their zeros from workgroups of
+// a fixed order (one sum's by a workgroup for each 256 columns).  The rows that no token is get their zeros from workgroups of
 // their own in the launch that sums, so each row of dw is written once.
 //
 // Measured: 16381 rows of 7168 FP32 values 160 us (5.9 TB/s); gradient of 8192

@@ -3,16 +3,16 @@
 // rows or across them (internal header of libfgs).
 //
 // A workgroup of NWM x NWN waves owns a BM x BN tile of C, each wave TI x TJ
-// accumulators of 32 x 32.  The contraction advances in steps of 64 values,
-// staged in LDS by copies that pass no register, into a ring of stages.  An
-// operand whose contraction runs along its rows is staged as BM (or BN) rows
-// of 128 bytes and read 16 bytes a lane; one whose contraction runs across its
-// rows as 64 rows of BM (or BN) values, read by the transposing loads, so no
+// accumulators of 32 x 32.  The contraction advances in steps of BK values (64
+// or 32), staged in LDS by copies that pass no register, into a ring of stages.
+// An operand whose contraction runs along its rows is staged as BM (or BN) rows
+// of 2 BK bytes and read 16 bytes a lane; one whose contraction runs across its
+// rows as BK rows of BM (or BN) values, read by the transposing loads, so no
 // operand has to be transposed in memory first.
 //
-// Bound by the matrix units: 8192 x 128000 over 4096 values 6.37 ms (1.35
+// Bound by the matrix units: 8192 x 128000 over 4096 values 6.47 ms (1.33
 // PFLOP/s, 73% busy, on a card where the library's product of 8192^3 reaches
-// 1.40), both operands read along their rows; 6.31 ms with both across them.
+// 1.38), both operands read along their rows; 6.38 ms with both across them.
 #pragma once
 
 #include <type_traits>

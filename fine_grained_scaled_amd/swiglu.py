@@ -90,6 +90,7 @@ class _Swiglu(torch.autograd.Function):
 def swiglu(gate_up: torch.Tensor, checkpoint: bool = True) -> torch.Tensor:
     """swiglu_fwd's h with autograd.  checkpoint: what the backward pass
     needs of gate_up is kept in 8 bits, so gate_up itself need not be
-    (False: it is kept as it is).  Layouts that the kernels do not read are
+    (False: it is kept as it is, and nothing is quantized, which is the form
+    for passes without a gradient).  Layouts that the kernels do not read are
     copied."""
     return _Swiglu.apply(gate_up, checkpoint)

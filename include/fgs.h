@@ -780,8 +780,9 @@ int fgs_swiglu_fwd(const void *gate_up, int64_t rows, int64_t inter, int64_t ld,
  *   at the values that q and scales stand for (gate_up NULL), or at gate_up
  *   itself (q NULL).  dgate_up: BF16 [rows x 2*inter], dense, FP32 products rounded
  *   once; for g < 0 so where |g| is below 174 and dh exp(g / 2)
- *   and u exp(g / 2) are normal FP32 numbers, and smaller or 0 elsewhere.  A tile
- *   that held NaN or Inf was kept as NaN: all of its gradients are NaN.
+ *   and u exp(g / 2) are normal FP32 numbers, and smaller or 0 elsewhere.  A half's
+ *   tile that held NaN or Inf was kept as NaN, and so are the gradients that its
+ *   values enter: dg and du of a tile of g, dg alone of a tile of u.
  */
 int fgs_swiglu_bwd(const void *dh, int64_t lddh, const void *gate_up, int64_t ld, const uint8_t *q, const float *scales,
                    int64_t rows, int64_t inter, void *dgate_up, void *stream);
